@@ -14,7 +14,7 @@ using infllmv2::Params;
 
 namespace {
 
-constexpr int kVersion = 100;  // 0.1.0
+constexpr int kVersion = 200;  // 0.2.0
 constexpr int kMaxDevices = 64;
 constexpr int kMaxLen = 1 << 28;
 constexpr int kMaxBlocks = 1024 * 32;  // blocks per sequence the top-k kernel holds in registers
@@ -161,6 +161,94 @@ DecodeWs decode_ws(int B, int n_draft, int Hkv, int d, int L_max, const Params& 
 
 int blocks_per_score_cta(const Params& p) { return 2048 / p.block_size; }
 
+// ---- rotary positions, drafts
+constexpr int kMaxHeads = 1 << 14;
+
+bool natural(const void* p, uintptr_t size) { return (reinterpret_cast<uintptr_t>(p) & (size - 1)) == 0; }
+
+// A tensor of rows `ld` elements apart, each `heads` heads of d.
+bool rows_ok(const void* p, int64_t ld, int heads, int d) {
+    return p != nullptr && aligned16(p) && ld >= static_cast<int64_t>(heads) * d && ld <= (int64_t{1} << 32);
+}
+
+bool ranges_apart(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x + na <= y || y + nb <= x;
+}
+
+struct RowSpan {
+    const void* p;
+    int64_t ld;
+    int width;  // elements of a row
+};
+// Whether two row tensors of elements of `es` bytes have no element in common (other columns of rows
+// with one stride are apart too).
+bool apart(const RowSpan& a, const RowSpan& b, int rows, int es) {
+    if (ranges_apart(a.p, (static_cast<size_t>(rows - 1) * a.ld + a.width) * es, b.p,
+                     (static_cast<size_t>(rows - 1) * b.ld + b.width) * es))
+        return true;
+    if (a.ld != b.ld) return false;
+    const int64_t stride = a.ld * es;
+    int64_t off = (static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p)) -
+                   static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.p))) % stride;
+    if (off < 0) off += stride;
+    return off >= static_cast<int64_t>(a.width) * es && off + static_cast<int64_t>(b.width) * es <= stride;
+}
+// An output may also be its own input.
+bool apart_or_same(const RowSpan& in, const RowSpan& out, int rows, int es) {
+    return (in.p == out.p && (in.ld == out.ld || rows == 1)) || apart(in, out, rows, es);
+}
+
+int check_rope(const infllmv2_rope_params* in, int d, infllmv2::RopeArgs* a) {
+    if (in == nullptr || !(in->attn_scale >= 0.f) || !isfinite(in->attn_scale)) return INFLLMV2_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return INFLLMV2_ERR_UNSUPPORTED;
+    if (in->rotary_dim < 2 || in->rotary_dim % 2 != 0 || in->rotary_dim > d || (in->interleaved & ~1) != 0)
+        return INFLLMV2_ERR_INVALID_ARG;
+    a->rot = in->rotary_dim;
+    a->interleaved = in->interleaved;
+    a->scale = in->attn_scale > 0.f ? in->attn_scale : 1.f;
+    return INFLLMV2_OK;
+}
+
+// Sizes of a chunk call; fills its rows (0: nothing to do).
+int check_chunk(const int32_t* cu_q, int B, int Tq, int total_q, int Hq, int L_max, infllmv2::RopeArgs* a) {
+    if (B < 0 || Tq < 0 || total_q < 0 || L_max <= 0 || L_max > kMaxLen || Hq > kMaxHeads) return INFLLMV2_ERR_INVALID_ARG;
+    a->rows = 0;
+    if (B == 0 || Tq == 0) return INFLLMV2_OK;
+    if (Tq > L_max) return INFLLMV2_ERR_INVALID_ARG;
+    if (cu_q == nullptr && static_cast<int64_t>(B) * Tq != total_q) return INFLLMV2_ERR_INVALID_ARG;
+    a->rows = total_q;
+    a->cu_q = cu_q;
+    a->B = B;
+    a->Tq = Tq;
+    a->L_max = L_max;
+    return INFLLMV2_OK;
+}
+
+// The bf16 q, K and V rows of a chunk or a draft tree, and the packed rotated q.
+int check_new_rows(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v, void* q_out,
+                   int Hq, int Hkv, int d, infllmv2::RopeArgs* a) {
+    const RowSpan qo{q_out, static_cast<int64_t>(Hq) * d, Hq * d};
+    if (!rows_ok(q, ld_q, Hq, d) || !rows_ok(k, ld_k, Hkv, d) || !rows_ok(v, ld_v, Hkv, d) ||
+        !rows_ok(q_out, qo.ld, Hq, d))
+        return INFLLMV2_ERR_INVALID_ARG;
+    if (!apart_or_same({q, ld_q, Hq * d}, qo, a->rows, 2) || !apart({k, ld_k, Hkv * d}, qo, a->rows, 2) ||
+        !apart({v, ld_v, Hkv * d}, qo, a->rows, 2))
+        return INFLLMV2_ERR_INVALID_ARG;
+    a->q = q;
+    a->k = k;
+    a->v = v;
+    a->q_out = q_out;
+    a->ld_q = ld_q;
+    a->ld_k = ld_k;
+    a->ld_v = ld_v;
+    a->ld_qo = qo.ld;
+    a->Hq = Hq;
+    a->Hk = a->Hv = a->Hkv = Hkv;
+    a->d = d;
+    return INFLLMV2_OK;
+}
+
 // ---- stage timing
 constexpr int kMaxStages = 8;
 struct ProfState {
@@ -210,6 +298,16 @@ void prof_mark(cudaStream_t stream, const char* stage) {
 namespace {
 using infllmv2::prof_begin;
 using infllmv2::prof_mark;
+
+int enqueue_rope(infllmv2::RopeArgs& a, void* stream) {
+    a.err = device_error_ptr();
+    if (a.err == nullptr) return INFLLMV2_ERR_CUDA;
+    a.stream = static_cast<cudaStream_t>(stream);
+    prof_begin(a.stream);
+    const cudaError_t e = infllmv2::launch_rope(a);
+    prof_mark(a.stream, "rope");
+    return cuda_status(e);
+}
 }  // namespace
 
 extern "C" {
@@ -222,7 +320,7 @@ const char* infllmv2_status_string(int status) {
         case INFLLMV2_ERR_WORKSPACE: return "workspace missing or too small";
         case INFLLMV2_ERR_CUDA: return "CUDA runtime error";
         case INFLLMV2_ERR_DEVICE_TIMEOUT: return "a bounded device-side wait ran out";
-        case INFLLMV2_ERR_DEVICE_INDEX: return "device saw kv_len or a selected block id out of range";
+        case INFLLMV2_ERR_DEVICE_INDEX: return "device saw kv_len, a selected block id or a draft tree out of range";
         case INFLLMV2_ERR_NOT_IMPLEMENTED: return "not implemented";
         default: return "unknown status";
     }
@@ -693,6 +791,234 @@ static int decode_impl(bool launch, const void* q, const void* k_cache, const vo
         return cuda_status(infllmv2::launch_tree_attention(da, idx, counts, stride));
     return cuda_status(
         infllmv2::launch_decode_attention(da, idx, counts, stride, reinterpret_cast<float*>(ws + w.part)));
+}
+
+int infllmv2_rope_freqs(int scaling, int rotary_dim, double base, double factor, int orig_len, double beta_fast,
+                        double beta_slow, const float* divisors, uint64_t* freqs_host, float* attn_scale) {
+    const double two_pi = 6.283185307179586476925286766559;
+    if (freqs_host == nullptr || rotary_dim < 2 || rotary_dim % 2 != 0 || rotary_dim > 1024) return INFLLMV2_ERR_INVALID_ARG;
+    if (!(base > 1.0) || !isfinite(base)) return INFLLMV2_ERR_INVALID_ARG;
+    if (scaling < INFLLMV2_ROPE_PLAIN || scaling > INFLLMV2_ROPE_DIVISORS) return INFLLMV2_ERR_UNSUPPORTED;
+    if (scaling != INFLLMV2_ROPE_PLAIN && (!(factor > 0.0) || !isfinite(factor))) return INFLLMV2_ERR_INVALID_ARG;
+    if (scaling == INFLLMV2_ROPE_NTK && rotary_dim <= 2) return INFLLMV2_ERR_INVALID_ARG;
+    if ((scaling == INFLLMV2_ROPE_YARN || scaling == INFLLMV2_ROPE_DIVISORS) && orig_len <= 1)
+        return INFLLMV2_ERR_INVALID_ARG;
+    if (scaling == INFLLMV2_ROPE_YARN && (!(beta_slow > 0.0) || !(beta_fast > beta_slow) || !isfinite(beta_fast)))
+        return INFLLMV2_ERR_INVALID_ARG;
+    const int half = rotary_dim / 2;
+    if (scaling == INFLLMV2_ROPE_DIVISORS) {
+        if (divisors == nullptr) return INFLLMV2_ERR_INVALID_ARG;
+        for (int i = 0; i < half; ++i)
+            if (!(divisors[i] > 0.f) || !isfinite(divisors[i])) return INFLLMV2_ERR_INVALID_ARG;
+    }
+    const double R = rotary_dim;
+    if (scaling == INFLLMV2_ROPE_NTK) base *= pow(factor, R / (R - 2.0));
+    double low = 0.0, high = 0.0;  // pairs below low keep theta, pairs from high on get theta / factor
+    if (scaling == INFLLMV2_ROPE_YARN) {
+        low = fmax(floor(R * log(orig_len / (beta_fast * two_pi)) / (2.0 * log(base))), 0.0);
+        high = fmin(ceil(R * log(orig_len / (beta_slow * two_pi)) / (2.0 * log(base))), R - 1.0);
+    }
+    for (int i = 0; i < half; ++i) {
+        double theta = pow(base, -2.0 * i / R);
+        if (scaling == INFLLMV2_ROPE_LINEAR) theta /= factor;
+        if (scaling == INFLLMV2_ROPE_YARN) {
+            const double ramp = fmin(fmax((i - low) / fmax(high - low, 0.001), 0.0), 1.0);
+            theta = theta / factor * ramp + theta * (1.0 - ramp);
+        }
+        if (scaling == INFLLMV2_ROPE_DIVISORS) theta /= divisors[i];
+        double whole;
+        const double turns = modf(theta / two_pi, &whole);
+        freqs_host[i] = static_cast<uint64_t>(ldexp(turns, 64));  // turns < 1: below 2^64
+    }
+    if (attn_scale != nullptr) {
+        double m = 1.0;
+        if (scaling == INFLLMV2_ROPE_YARN && factor > 1.0) m = 0.1 * log(factor) + 1.0;
+        if (scaling == INFLLMV2_ROPE_DIVISORS && factor > 1.0) m = sqrt(1.0 + log(factor) / log(static_cast<double>(orig_len)));
+        *attn_scale = static_cast<float>(m);
+    }
+    return INFLLMV2_OK;
+}
+
+int infllmv2_rope(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const int32_t* pos, const uint64_t* freqs,
+                  int rows, int Hq, int Hk, int d, int dtype, int transposed, void* q_out, int64_t ld_qo, void* k_out,
+                  int64_t ld_ko, const infllmv2_rope_params* rope, void* stream) {
+    infllmv2::RopeArgs a{};
+    if (int rc = check_rope(rope, d, &a)) return rc;
+    if (dtype != INFLLMV2_BF16 && dtype != INFLLMV2_FP32) return INFLLMV2_ERR_UNSUPPORTED;
+    if (rows < 0 || Hq <= 0 || Hk < 0 || Hq > kMaxHeads || Hk > kMaxHeads) return INFLLMV2_ERR_INVALID_ARG;
+    if (rows == 0) return INFLLMV2_OK;
+    const int es = dtype == INFLLMV2_FP32 ? 4 : 2;
+    if (!pos || !freqs || !natural(pos, 4) || !natural(freqs, 8)) return INFLLMV2_ERR_INVALID_ARG;
+    if (!rows_ok(q, ld_q, Hq, d) || !rows_ok(q_out, ld_qo, Hq, d)) return INFLLMV2_ERR_INVALID_ARG;
+    const RowSpan qi{q, ld_q, Hq * d}, qo{q_out, ld_qo, Hq * d}, ki{k, ld_k, Hk * d}, ko{k_out, ld_ko, Hk * d};
+    if (!apart_or_same(qi, qo, rows, es)) return INFLLMV2_ERR_INVALID_ARG;
+    if ((k == nullptr) != (Hk == 0) || (k_out == nullptr) != (Hk == 0)) return INFLLMV2_ERR_INVALID_ARG;
+    if (Hk > 0 && (!rows_ok(k, ld_k, Hk, d) || !rows_ok(k_out, ld_ko, Hk, d) || !apart_or_same(ki, ko, rows, es) ||
+                   !apart(qi, ko, rows, es) || !apart(ki, qo, rows, es) || !apart(qo, ko, rows, es)))
+        return INFLLMV2_ERR_INVALID_ARG;
+    a.form = infllmv2::kRopeRows;
+    a.q = q;
+    a.k = k;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.ld_q = ld_q;
+    a.ld_qo = ld_qo;
+    a.ld_k = Hk > 0 ? ld_k : 0;
+    a.ld_ko = Hk > 0 ? ld_ko : 0;
+    a.pos = pos;
+    a.freqs = reinterpret_cast<const unsigned long long*>(freqs);
+    a.rows = rows;
+    a.Hq = Hq;
+    a.Hk = a.Hkv = Hk;
+    a.d = d;
+    a.transposed = transposed != 0;
+    a.in_f32 = a.out_f32 = dtype == INFLLMV2_FP32;
+    return enqueue_rope(a, stream);
+}
+
+int infllmv2_rope_append(const void* q, int64_t ld_q, const void* k_new, int64_t ld_k, const void* v_new, int64_t ld_v,
+                         void* q_out, void* k_cache, void* v_cache, const int32_t* kv_len, const int32_t* cu_q,
+                         const uint64_t* freqs, int B, int Tq, int total_q, int Hq, int Hkv, int d, int L_max,
+                         const infllmv2_rope_params* rope, void* stream) {
+    infllmv2::RopeArgs a{};
+    if (int rc = check_rope(rope, d, &a)) return rc;
+    if (int rc = check_heads(Hq, Hkv, d)) return rc;
+    if (int rc = check_chunk(cu_q, B, Tq, total_q, Hq, L_max, &a)) return rc;
+    if (a.rows == 0) return INFLLMV2_OK;
+    if (int rc = check_new_rows(q, ld_q, k_new, ld_k, v_new, ld_v, q_out, Hq, Hkv, d, &a)) return rc;
+    if (!k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)) return INFLLMV2_ERR_INVALID_ARG;
+    if (!kv_len || !natural(kv_len, 4) || !natural(cu_q, 4) || !freqs || !natural(freqs, 8)) return INFLLMV2_ERR_INVALID_ARG;
+    a.form = infllmv2::kRopeChunk;
+    a.k_out = k_cache;
+    a.v_out = v_cache;
+    a.kv_len = kv_len;
+    a.freqs = reinterpret_cast<const unsigned long long*>(freqs);
+    return enqueue_rope(a, stream);
+}
+
+int infllmv2_rope_append_bwd(const float* dq, const float* dk, const float* dv, void* dq_out, int64_t ld_dq, void* dk_out,
+                             int64_t ld_dk, void* dv_out, int64_t ld_dv, const int32_t* kv_len, const int32_t* cu_q,
+                             const uint64_t* freqs, int B, int Tq, int total_q, int Hq, int Hkv, int d, int L_max,
+                             int dtype, const infllmv2_rope_params* rope, void* stream) {
+    infllmv2::RopeArgs a{};
+    if (int rc = check_rope(rope, d, &a)) return rc;
+    if (int rc = check_heads(Hq, Hkv, d)) return rc;
+    if (dtype != INFLLMV2_BF16 && dtype != INFLLMV2_FP32) return INFLLMV2_ERR_UNSUPPORTED;
+    if (int rc = check_chunk(cu_q, B, Tq, total_q, Hq, L_max, &a)) return rc;
+    if (a.rows == 0) return INFLLMV2_OK;
+    const int64_t ld = static_cast<int64_t>(Hq) * d;
+    if (!rows_ok(dq, ld, Hq, d) || !rows_ok(dq_out, ld_dq, Hq, d) || !rows_ok(dk_out, ld_dk, Hkv, d) ||
+        !rows_ok(dv_out, ld_dv, Hkv, d))
+        return INFLLMV2_ERR_INVALID_ARG;
+    const int es = dtype == INFLLMV2_FP32 ? 4 : 2;
+    const RowSpan qo{dq_out, ld_dq, Hq * d}, ko{dk_out, ld_dk, Hkv * d}, vo{dv_out, ld_dv, Hkv * d};
+    const size_t n_dq = static_cast<size_t>(a.rows) * ld * 4;
+    for (const RowSpan* o : {&qo, &ko, &vo}) {
+        if (o == &qo && dtype == INFLLMV2_FP32 && apart_or_same({dq, ld, Hq * d}, qo, a.rows, es)) continue;
+        if (!ranges_apart(dq, n_dq, o->p, (static_cast<size_t>(a.rows - 1) * o->ld + o->width) * es))
+            return INFLLMV2_ERR_INVALID_ARG;
+    }
+    if (!apart(qo, ko, a.rows, es) || !apart(qo, vo, a.rows, es) || !apart(ko, vo, a.rows, es))
+        return INFLLMV2_ERR_INVALID_ARG;
+    if (!dk || !dv || !aligned16(dk) || !aligned16(dv)) return INFLLMV2_ERR_INVALID_ARG;
+    if (!kv_len || !natural(kv_len, 4) || !natural(cu_q, 4) || !freqs || !natural(freqs, 8)) return INFLLMV2_ERR_INVALID_ARG;
+    a.form = infllmv2::kRopeChunkBack;
+    a.q = dq;
+    a.k = dk;
+    a.v = dv;
+    a.q_out = dq_out;
+    a.k_out = dk_out;
+    a.v_out = dv_out;
+    a.ld_q = ld;
+    a.ld_qo = ld_dq;
+    a.ld_ko = ld_dk;
+    a.ld_vo = ld_dv;
+    a.kv_len = kv_len;
+    a.freqs = reinterpret_cast<const unsigned long long*>(freqs);
+    a.Hq = Hq;
+    a.Hk = a.Hv = a.Hkv = Hkv;
+    a.d = d;
+    a.transposed = 1;
+    a.in_f32 = 1;
+    a.out_f32 = dtype == INFLLMV2_FP32;
+    return enqueue_rope(a, stream);
+}
+
+int infllmv2_rope_drafts(const void* q, int64_t ld_q, const void* k_new, int64_t ld_k, const void* v_new, int64_t ld_v,
+                         void* q_out, void* draft_k, void* draft_v, const int32_t* kv_len, const uint64_t* tree_mask,
+                         const uint64_t* freqs, int B, int n_draft, int Hq, int Hkv, int d,
+                         const infllmv2_rope_params* rope, void* stream) {
+    infllmv2::RopeArgs a{};
+    if (int rc = check_rope(rope, d, &a)) return rc;
+    if (int rc = check_heads(Hq, Hkv, d)) return rc;
+    if (B < 0 || n_draft < 0 || Hq > kMaxHeads) return INFLLMV2_ERR_INVALID_ARG;
+    if (n_draft > 64) return INFLLMV2_ERR_UNSUPPORTED;
+    if (B == 0 || n_draft == 0) return INFLLMV2_OK;
+    if (static_cast<int64_t>(B) * n_draft > INT32_MAX) return INFLLMV2_ERR_INVALID_ARG;
+    a.rows = B * n_draft;
+    if (int rc = check_new_rows(q, ld_q, k_new, ld_k, v_new, ld_v, q_out, Hq, Hkv, d, &a)) return rc;
+    if (!draft_k || !draft_v || !aligned16(draft_k) || !aligned16(draft_v)) return INFLLMV2_ERR_INVALID_ARG;
+    if (!kv_len || !natural(kv_len, 4) || !tree_mask || !natural(tree_mask, 8) || !freqs || !natural(freqs, 8))
+        return INFLLMV2_ERR_INVALID_ARG;
+    a.form = infllmv2::kRopeDrafts;
+    a.k_out = draft_k;
+    a.v_out = draft_v;
+    a.kv_len = kv_len;
+    a.tree_mask = reinterpret_cast<const unsigned long long*>(tree_mask);
+    a.freqs = reinterpret_cast<const unsigned long long*>(freqs);
+    a.B = B;
+    a.Tq = a.L_max = n_draft;
+    return enqueue_rope(a, stream);
+}
+
+int infllmv2_verify(const int32_t* tokens, const uint64_t* tree_mask, const int32_t* n_nodes, const void* target,
+                    const void* draft, const float* u, const int32_t* kv_len, int B, int n_draft, int V, int dtype,
+                    int replace, int32_t* path, int32_t* n_path, int32_t* out_tokens, int32_t* kv_len_out,
+                    void* stream) {
+    if (B < 0 || n_draft < 0 || V <= 0) return INFLLMV2_ERR_INVALID_ARG;
+    if (n_draft > 64 || V > (1 << 24) || (dtype != INFLLMV2_BF16 && dtype != INFLLMV2_FP32)) return INFLLMV2_ERR_UNSUPPORTED;
+    if (B == 0 || n_draft == 0) return INFLLMV2_OK;
+    if (B > (1 << 24)) return INFLLMV2_ERR_INVALID_ARG;
+    if (!tokens || !target || !u || !path || !n_path || !out_tokens || (kv_len == nullptr) != (kv_len_out == nullptr))
+        return INFLLMV2_ERR_INVALID_ARG;
+    if (!aligned16(target) || !aligned16(draft) || !natural(tokens, 4) || !natural(tree_mask, 8) || !natural(n_nodes, 4) ||
+        !natural(u, 4) || !natural(kv_len, 4) || !natural(path, 4) || !natural(n_path, 4) || !natural(out_tokens, 4) ||
+        !natural(kv_len_out, 4))
+        return INFLLMV2_ERR_INVALID_ARG;
+    int* err = device_error_ptr();
+    if (err == nullptr) return INFLLMV2_ERR_CUDA;
+    const infllmv2::VerifyArgs a{tokens, reinterpret_cast<const unsigned long long*>(tree_mask), n_nodes, target, draft, u,
+                                 kv_len, B, n_draft, V, dtype == INFLLMV2_BF16, replace != 0, path, n_path, out_tokens,
+                                 kv_len_out, err, static_cast<cudaStream_t>(stream)};
+    prof_begin(a.stream);
+    const cudaError_t e = infllmv2::launch_verify(a);
+    prof_mark(a.stream, "verify");
+    return cuda_status(e);
+}
+
+int infllmv2_commit(const void* draft_k, const void* draft_v, const int32_t* path, const int32_t* n_path, void* k_cache,
+                    void* v_cache, void* kernel_cache, const int32_t* kv_len, int B, int n_draft, int Hkv, int d, int L_max,
+                    int M_max, const infllmv2_params* params, void* stream) {
+    Params p;
+    if (int rc = check_params(params, d, &p)) return rc;
+    if (d != 64 && d != 128) return INFLLMV2_ERR_UNSUPPORTED;
+    if (B < 0 || n_draft < 0 || Hkv <= 0 || L_max <= 0 || L_max > kMaxLen || M_max < 0) return INFLLMV2_ERR_INVALID_ARG;
+    if (n_draft > 64) return INFLLMV2_ERR_UNSUPPORTED;
+    if (B == 0 || n_draft == 0) return INFLLMV2_OK;
+    if (static_cast<int64_t>(B) * Hkv > INT32_MAX) return INFLLMV2_ERR_INVALID_ARG;
+    if (!draft_k || !draft_v || !path || !n_path || !k_cache || !v_cache || !kv_len || (M_max > 0 && !kernel_cache))
+        return INFLLMV2_ERR_INVALID_ARG;
+    if (!aligned16(draft_k) || !aligned16(draft_v) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        !aligned16(kernel_cache) || !natural(path, 4) || !natural(n_path, 4) || !natural(kv_len, 4))
+        return INFLLMV2_ERR_INVALID_ARG;
+    int* err = device_error_ptr();
+    if (err == nullptr) return INFLLMV2_ERR_CUDA;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    prof_begin(st);
+    const cudaError_t e = infllmv2::launch_commit(draft_k, draft_v, path, n_path, k_cache, v_cache, kernel_cache, kv_len, B,
+                                                  n_draft, Hkv, L_max, M_max, d, p.kernel_size, p.kernel_stride, err, st);
+    prof_mark(st, "commit");
+    return cuda_status(e);
 }
 
 }  // extern "C"

@@ -91,6 +91,52 @@ struct BwdArgs {
     cudaStream_t stream;
 };
 
+// Rotary positions (rope.cu).  Rows of heads are [rows][ld] with head h at h*d; caches (and draft
+// buffers, L_max = n_draft rows) are [B, Hkv, L_max, d].
+enum : int {
+    kRopeRows = 0,       // q, k rows -> rows, at explicit positions
+    kRopeChunk = 1,      // a chunk's q, k, v rows -> q rows and the caches
+    kRopeChunkBack = 2,  // gradients: q rows and cache rows -> rows
+    kRopeDrafts = 3      // a draft tree's q, k, v rows -> q rows and the draft buffers
+};
+struct RopeArgs {
+    int form;
+    const void *q, *k, *v;
+    void *q_out, *k_out, *v_out;
+    long long ld_q, ld_k, ld_v, ld_qo, ld_ko, ld_vo;  // row strides in elements (0 where not a row tensor)
+    const int* pos;
+    const int* kv_len;
+    const int* cu_q;
+    const unsigned long long* tree_mask;
+    const unsigned long long* freqs;  // [rot / 2] turns per position, in units of 2^-64
+    int rows, B, Tq, Hq, Hk, Hv, Hkv, d, L_max;
+    int rot, interleaved, transposed;
+    float scale;
+    int in_f32, out_f32;
+    int* err;
+    cudaStream_t stream;
+};
+cudaError_t launch_rope(const RopeArgs& a);
+
+// Verification of a draft tree against the target's probabilities (verify.cu).
+struct VerifyArgs {
+    const int* tokens;
+    const unsigned long long* tree_mask;
+    const int* n_nodes;
+    const void* target;
+    const void* draft;
+    const float* u;
+    const int* kv_len;
+    int B, n, V, bf16, replace;
+    int* path;
+    int* n_path;
+    int* out_tokens;
+    int* kv_len_out;
+    int* err;
+    cudaStream_t stream;
+};
+cudaError_t launch_verify(const VerifyArgs& a);
+
 // 2-D bf16 tensor map over `rows` rows of `inner` elements (row stride inner*2 bytes) with
 // box [box_rows][box_inner] and the 128-byte swizzle; false if the driver refuses.
 bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_inner,
@@ -110,6 +156,9 @@ void prof_mark(cudaStream_t stream, const char* stage);
 cudaError_t launch_append(const void* k_new, const void* v_new, void* k_cache, void* v_cache, void* kernel_cache,
                           const int* kv_len, int B, int Hkv, int L_max, int M_max, int d, int c, int s, int* err,
                           cudaStream_t stream);
+cudaError_t launch_commit(const void* draft_k, const void* draft_v, const int* path, const int* n_path, void* k_cache,
+                          void* v_cache, void* kernel_cache, const int* kv_len, int B, int n_draft, int Hkv, int L_max,
+                          int M_max, int d, int c, int s, int* err, cudaStream_t stream);
 cudaError_t launch_kernel_pool_seq(const void* k_cache, void* kernel_cache, const int* kv_len, const SeqMap& sm,
                                    int B, int Hkv, int L_max, int M_max, int d, int c, int s, int* err,
                                    cudaStream_t stream);

@@ -134,6 +134,73 @@ cudaError_t launch_append(const void* k_new, const void* v_new, void* k_cache, v
     return cudaGetLastError();
 }
 
+// Commit of accepted drafts ("MiniCPM4: 如何在手机电脑上高效运行大语言模型", section 1.1, tree-speculative
+// decoding; static caches of "CPM.cu：端侧大模型推理的 CUDA 加速引擎", section 4): the K and V of the
+// path's drafts into the last n_path rows of each sequence's caches, and the semantic kernels that
+// these tokens complete, as kernel_pool_kernel computes them.  CTAs of blockIdx.y 0 copy; each other
+// one pools one kernel, taking the rows being committed from the draft buffer, so that no CTA reads
+// what another writes.
+template <int D>
+__global__ void __launch_bounds__(2 * D) commit_kernel(
+    const __nv_bfloat16* __restrict__ dk, const __nv_bfloat16* __restrict__ dv, const int* __restrict__ path,
+    const int* __restrict__ n_path, __nv_bfloat16* k, __nv_bfloat16* __restrict__ v, __nv_bfloat16* __restrict__ kern,
+    const int* __restrict__ kv_len, int n, int Hkv, int L_max, int M_max, int c, int s, int* __restrict__ err) {
+    constexpr int kChunks = D / 8;
+    __shared__ int path_s[64];
+    const int bg = blockIdx.x, b = bg / Hkv, tid = threadIdx.x;
+    const int m = n_path[b], L = kv_len[b];
+    const int j_last = L >= c ? (L - c) / s : -1;
+    const int num = L - m - c + 1;  // kernels ending at or after the first committed token
+    const int j_first = num <= 0 ? 0 : (num + s - 1) / s;
+    bool bad = m < 0 || m > n || L < m || L > L_max || (m > 0 && j_last >= j_first && j_last >= M_max);
+    if (!bad && tid < m) {
+        const int i = path[static_cast<size_t>(b) * n + tid];
+        path_s[tid] = i;
+        bad = i < 0 || i >= n;
+    }
+    if (__syncthreads_or(bad)) {
+        if (tid == 0 && blockIdx.y == 0) raise_error(err, kDevErrIndex);
+        return;
+    }
+    const size_t src0 = static_cast<size_t>(bg) * n, row0 = static_cast<size_t>(bg) * L_max;
+    if (blockIdx.y == 0) {
+        for (int i = tid; i < m * kChunks; i += 2 * D) {
+            const int t = i / kChunks, ch = i % kChunks;
+            const size_t from = (src0 + path_s[t]) * kChunks + ch, to = (row0 + (L - m) + t) * kChunks + ch;
+            reinterpret_cast<uint4*>(k)[to] = ldg_v4(reinterpret_cast<const uint4*>(dk) + from);
+            reinterpret_cast<uint4*>(v)[to] = ldg_v4(reinterpret_cast<const uint4*>(dv) + from);
+        }
+        return;
+    }
+    const int j = j_first + static_cast<int>(blockIdx.y) - 1;
+    if (m == 0 || j > j_last) return;
+    const int ch = tid / kMeanLanes, ln = tid % kMeanLanes;
+    const uint4 r = exact_mean_rows(c, ln, [&](int i) {
+        const int x = j * s + i, t = x - (L - m);  // t at or past 0: a committed row
+        return t >= 0 ? ldg_v4(reinterpret_cast<const uint4*>(dk) + (src0 + path_s[t]) * kChunks + ch)
+                      : ldg_v4(reinterpret_cast<const uint4*>(k) + (row0 + x) * kChunks + ch);
+    });
+    if (ln == 0) reinterpret_cast<uint4*>(kern)[(static_cast<size_t>(bg) * M_max + j) * kChunks + ch] = r;
+}
+
+cudaError_t launch_commit(const void* draft_k, const void* draft_v, const int* path, const int* n_path, void* k_cache,
+                          void* v_cache, void* kernel_cache, const int* kv_len, int B, int n_draft, int Hkv, int L_max,
+                          int M_max, int d, int c, int s, int* err, cudaStream_t stream) {
+    const dim3 grid(B * Hkv, 1 + (n_draft - 1) / s + 1);  // most kernels that n_draft tokens complete
+    const auto* dk = static_cast<const __nv_bfloat16*>(draft_k);
+    const auto* dv = static_cast<const __nv_bfloat16*>(draft_v);
+    auto* kc = static_cast<__nv_bfloat16*>(k_cache);
+    auto* vc = static_cast<__nv_bfloat16*>(v_cache);
+    auto* kp = static_cast<__nv_bfloat16*>(kernel_cache);
+    if (d == 128)
+        commit_kernel<128><<<grid, 256, 0, stream>>>(dk, dv, path, n_path, kc, vc, kp, kv_len, n_draft, Hkv, L_max, M_max,
+                                                     c, s, err);
+    else
+        commit_kernel<64><<<grid, 128, 0, stream>>>(dk, dv, path, n_path, kc, vc, kp, kv_len, n_draft, Hkv, L_max, M_max,
+                                                    c, s, err);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_kernel_pool(const void* k_cache, void* kernel_cache, int B, int Hkv, int L_max,
                                int M_max, int d, int j_first, int n_new, int c, int s,
                                cudaStream_t stream) {

@@ -48,17 +48,17 @@ __device__ __forceinline__ uint32_t bf16_of_ratio(unsigned long long A, int c, i
 }
 
 // Exact mean of the c rows of one 8-element slice; lane ln (of the 16 aligned lanes sharing the
-// slice) loads rows ln, ln + 16, ...; row `sub_row` is taken from `sub_val` instead of memory.
-// Every lane of the group returns the 8 bf16 results, packed.
-__device__ __forceinline__ uint4 exact_mean_slice(const uint4* src, size_t row_stride, int c, int ln, int sub_row,
-                                                  uint4 sub_val) {
+// slice) takes rows ln, ln + 16, ... from row(i).  Every lane of the group returns the 8 bf16
+// results, packed.
+template <typename RowOf>
+__device__ __forceinline__ uint4 exact_mean_rows(int c, int ln, RowOf row) {
     uint32_t w[kMeanRows][4];
     const int n_u = (c + kMeanLanes - 1) / kMeanLanes;  // row rounds any lane of the group has
 #pragma unroll
     for (int u = 0; u < kMeanRows; ++u) {
         const int i = ln + kMeanLanes * u;
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (u < n_u && i < c) x = i == sub_row ? sub_val : ldg_v4(src + static_cast<size_t>(i) * row_stride);
+        if (u < n_u && i < c) x = row(i);
         w[u][0] = x.x;
         w[u][1] = x.y;
         w[u][2] = x.z;
@@ -115,6 +115,14 @@ __device__ __forceinline__ uint4 exact_mean_slice(const uint4* src, size_t row_s
     for (int e = 0; e < 4; ++e)
         out[e] = __shfl_sync(0xffffffffu, bits, g0 + 2 * e) | (__shfl_sync(0xffffffffu, bits, g0 + 2 * e + 1) << 16);
     return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// The same with the rows in memory, row_stride apart, but row `sub_row` taken from `sub_val`.
+__device__ __forceinline__ uint4 exact_mean_slice(const uint4* src, size_t row_stride, int c, int ln, int sub_row,
+                                                  uint4 sub_val) {
+    return exact_mean_rows(c, ln, [&](int i) {
+        return i == sub_row ? sub_val : ldg_v4(src + static_cast<size_t>(i) * row_stride);
+    });
 }
 
 }  // namespace infllmv2

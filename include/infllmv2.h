@@ -358,6 +358,172 @@ int infllmv2_decode_step(const void* q, const void* k_new, const void* v_new, vo
                          size_t ws_bytes, const infllmv2_params* params, void* stream);
 
 /*
+ * Rotary positions.  The method's q and K carry their positions when they reach
+ * the scores and the caches; these entry points put them on.  Pair i of a head
+ * (i < rotary_dim / 2) is elements i and rotary_dim/2 + i, or, interleaved, 2i
+ * and 2i + 1.  In the row at position x it turns by x * theta_i:
+ *   y_a = attn_scale (a cos - b sin),  y_b = attn_scale (a sin + b cos)
+ * in fp32, rounded once; elements from rotary_dim on are copied bit for bit.
+ */
+typedef struct infllmv2_rope_params {
+    int32_t rotary_dim;   /* leading elements of a head that turn: even, 2 .. d      */
+    int32_t interleaved;  /* 0: pairs (i, rotary_dim/2 + i); 1: pairs (2i, 2i + 1)    */
+    float attn_scale;     /* factor on the rotated elements; 0 selects 1             */
+} infllmv2_rope_params;
+
+/* Scalings for contexts longer than the trained one (infllmv2_rope_freqs). */
+enum {
+    INFLLMV2_ROPE_PLAIN = 0,   /* theta_i = base^(-2i / rotary_dim)                        */
+    INFLLMV2_ROPE_LINEAR = 1,  /* theta_i / factor (positions squeezed)                   */
+    INFLLMV2_ROPE_NTK = 2,     /* plain with base * factor^(rotary_dim / (rotary_dim-2))  */
+    INFLLMV2_ROPE_YARN = 3,    /* by wavelength: theta_i where a pair turns more than
+                                  beta_fast times within orig_len tokens, theta_i / factor
+                                  where less than beta_slow times, a ramp over i between;
+                                  attn_scale = 0.1 ln(factor) + 1 (1 for factor <= 1)     */
+    INFLLMV2_ROPE_DIVISORS = 4 /* theta_i / divisors[i] (searched per-pair factors);
+                                  attn_scale = sqrt(1 + ln(factor) / ln(orig_len)), 1 for
+                                  factor <= 1                                             */
+};
+
+/* Types of the tensors that take a dtype argument. */
+enum { INFLLMV2_BF16 = 0, INFLLMV2_FP32 = 1 };
+
+/*
+ * Host helper: the table of frequencies that the entry points below read from
+ * device memory.  freqs_host[i] = floor(frac(theta_i / 2 pi) * 2^64), the turns
+ * per position in units of 2^-64: position times it, modulo 2^64, is the
+ * fraction of a turn for every int32 position, so far positions lose nothing.
+ * Writes rotary_dim / 2 entries and, when attn_scale is not NULL, the scaling's
+ * factor.  base > 1; factor > 0 is read by every scaling but PLAIN; orig_len > 1
+ * by YARN and DIVISORS; beta_fast > beta_slow > 0 by YARN; divisors
+ * [rotary_dim / 2], each > 0, by DIVISORS.  NTK needs rotary_dim > 2.
+ */
+int infllmv2_rope_freqs(int scaling, int rotary_dim, double base, double factor, int orig_len, double beta_fast,
+                        double beta_slow, const float* divisors, uint64_t* freqs_host, float* attn_scale);
+
+/*
+ * Rotary positions of q and K rows at explicit positions.  Row r of q is Hq
+ * heads of d elements at q + r*ld_q (likewise the others; ld in elements, at
+ * least heads * d, so slices of a fused projection are taken as they are).
+ *   pos     [rows] device int32, any value
+ *   freqs   [rotary_dim / 2] device uint64 (infllmv2_rope_freqs)
+ *   dtype   of q, k and the outputs: INFLLMV2_BF16 or INFLLMV2_FP32
+ *   transposed != 0: the transpose (opposite angles, the same factor): the
+ *           gradient of the inputs from the gradient of the outputs.
+ * k may be NULL with k_out NULL and Hk 0.  An output may be its input (the same
+ * pointer and ld); any other overlap is refused (here and below: of row tensors
+ * with each other; caches and draft buffers overlap nothing else).  d 64 or 128.
+ */
+int infllmv2_rope(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const int32_t* pos, const uint64_t* freqs,
+                  int rows, int Hq, int Hk, int d, int dtype, int transposed, void* q_out, int64_t ld_qo, void* k_out,
+                  int64_t ld_ko, const infllmv2_rope_params* rope, void* stream);
+
+/*
+ * A chunk into the caches: q rotated to q_out, K rotated into k_cache and V
+ * copied into v_cache, each token at its position.  The chunk is the last tokens
+ * of each sequence, as for the attention calls:
+ *   cu_q == NULL: Tq tokens per sequence, rows b*Tq + t at positions
+ *                 kv_len[b] - Tq + t (total_q is B*Tq);
+ *   cu_q != NULL: packed, rows cu_q[b] + t at kv_len[b] - len_b + t, len_b at
+ *                 most Tq; rows from cu_q[B] to total_q are left as they are.
+ * q [total_q rows of ld_q], k_new, v_new [rows of ld_k, ld_v] bf16; q_out
+ * [total_q, Hq, d] packed, q itself when ld_q = Hq*d; caches [B, Hkv, L_max, d].
+ * Kernels that the chunk completes are pooled by infllmv2_kernel_pool(_varlen).
+ * Device errors (kv_len[b] below the chunk's length or past L_max, a length
+ * outside [0, Tq], cu_q[B] past total_q) set the error word; that sequence is
+ * skipped.
+ */
+int infllmv2_rope_append(const void* q, int64_t ld_q, const void* k_new, int64_t ld_k, const void* v_new, int64_t ld_v,
+                         void* q_out, void* k_cache, void* v_cache, const int32_t* kv_len, const int32_t* cu_q,
+                         const uint64_t* freqs, int B, int Tq, int total_q, int Hq, int Hkv, int d, int L_max,
+                         const infllmv2_rope_params* rope, void* stream);
+
+/*
+ * The gradient of infllmv2_rope_append: from the fp32 gradients that
+ * infllmv2_sparse_attn_bwd gives -- dq [total_q, Hq, d] of the rotated q, dk and
+ * dv [B, Hkv, L_max, d] of the caches -- those of the chunk's q, K and V rows
+ * before rotation, dq_out, dk_out, dv_out (row strides ld_*, as above; dtype
+ * INFLLMV2_BF16 or INFLLMV2_FP32).  dq_out may be dq (fp32, ld_dq = Hq*d).
+ * Rows of skipped sequences and behind the last sequence are left as they are.
+ */
+int infllmv2_rope_append_bwd(const float* dq, const float* dk, const float* dv, void* dq_out, int64_t ld_dq, void* dk_out,
+                             int64_t ld_dk, void* dv_out, int64_t ld_dv, const int32_t* kv_len, const int32_t* cu_q,
+                             const uint64_t* freqs, int B, int Tq, int total_q, int Hq, int Hkv, int d, int L_max,
+                             int dtype, const infllmv2_rope_params* rope, void* stream);
+
+/*
+ * A draft tree's q, K and V as infllmv2_decode takes them.  Draft i of sequence
+ * b sits depth - 1 positions after the committed tokens, depth = the bits of
+ * tree_mask[b, i] (its ancestors and itself; an empty mask counts as 1):
+ * position kv_len[b] + depth - 1.  q, k_new, v_new are rows b*n_draft + i of
+ * ld_q, ld_k, ld_v elements; q_out [B, n_draft, Hq, d] (q itself when
+ * ld_q = Hq*d), draft_k and draft_v [B, Hkv, n_draft, d].  A kv_len outside
+ * [0, 2^28] sets the error word; that sequence is skipped.
+ */
+int infllmv2_rope_drafts(const void* q, int64_t ld_q, const void* k_new, int64_t ld_k, const void* v_new, int64_t ld_v,
+                         void* q_out, void* draft_k, void* draft_v, const int32_t* kv_len, const uint64_t* tree_mask,
+                         const uint64_t* freqs, int B, int n_draft, int Hq, int Hkv, int d,
+                         const infllmv2_rope_params* rope, void* stream);
+
+/*
+ * Verification of a draft tree ([MiniCPM4-1.1] tree-speculative decoding) by
+ * recursive rejection sampling, from given random numbers.  Node 0 is the tree's
+ * root, the token sampled last: it always stands.  Node i's parent is the
+ * ancestor whose mask is tree_mask[b, i] without bit i; ancestors come before
+ * their descendants.  Rows of probabilities:
+ *   target [B, n_draft, V]: row i is the target's distribution after node i
+ *   draft  [B, n_draft, V]: row i is the distribution node i's children were
+ *          drawn from; only rows of nodes with children are read.  NULL: the
+ *          drafts were chosen, not drawn (a child's own probability is then 1).
+ * From the root down, the children x of a node (by index) are tried in turn with
+ * w = p, Z = 1, R = 1 (p, q the node's target and draft rows):
+ *   x stands iff u[x] Z q(x) < w(x) R.  Otherwise w(y) becomes
+ *   max(w(y) - (Z/R) q(y), 0) for every token y, Z the sum of w, and, without
+ *   replacement (replace == 0), R loses q(x); with R <= 0 nothing changes.
+ *   draft == NULL: x stands iff u[x] Z < w(x); otherwise Z loses w(x), w(x) = 0.
+ * The first child that stands is the next node; where none does, the last token
+ * is the first one whose running sum of w passes u[0] * (sum of w), or of p when
+ * w has nothing left.  Decisions are taken in 64 bits, sums in units of 2^-62.
+ *   tokens    [B, n_draft] int32; a root's is not read
+ *   tree_mask [B, n_draft], NULL: a chain (node i's parent is i - 1)
+ *   n_nodes   [B] int32 in [0, n_draft], nodes in use (0: the sequence is idle);
+ *             NULL: n_draft everywhere
+ *   u         [B, n_draft] fp32 in [0, 1): u[b, i] tries node i, u[b, 0] draws
+ *   dtype     of target and draft: INFLLMV2_FP32 or INFLLMV2_BF16
+ * Out: path [B, n_draft], the nodes that stand, from the root, then -1; n_path
+ * [B] their number; out_tokens [B, n_draft], the n_path[b] new tokens (the
+ * path's behind the root, then the one drawn), then -1; and, with kv_len given,
+ * kv_len_out[b] = kv_len[b] + n_path[b] (the lengths with the path committed;
+ * kv_len_out may be kv_len; both NULL or neither).
+ * Probabilities: NaN and values below 0 are read as 0, values above 1 as 1.
+ * Device errors (masks that are no tree, a token outside [0, V), n_nodes out of
+ * range, a row whose sum is 0 or above 2) set the error word; that sequence's
+ * outputs are those of an idle one: n_path 0, -1 elsewhere, kv_len unchanged.
+ * Needs no workspace.  n_draft <= 64, V <= 2^24.
+ */
+int infllmv2_verify(const int32_t* tokens, const uint64_t* tree_mask, const int32_t* n_nodes, const void* target,
+                    const void* draft, const float* u, const int32_t* kv_len, int B, int n_draft, int V, int dtype,
+                    int replace, int32_t* path, int32_t* n_path, int32_t* out_tokens, int32_t* kv_len_out,
+                    void* stream);
+
+/*
+ * Commit of a verified path: the accepted drafts' K and V become the last
+ * n_path[b] tokens of each sequence, and the semantic kernels that they complete
+ * are pooled exactly as infllmv2_kernel_pool does (one launch).  kv_len counts
+ * the committed tokens (infllmv2_verify's kv_len_out):
+ *   cache row kv_len[b] - n_path[b] + t = draft row path[b, t],  t < n_path[b]
+ *   draft_k, draft_v [B, Hkv, n_draft, d] bf16, as for infllmv2_decode, and not
+ *   overlapping the caches; path [B, n_draft], n_path [B] device int32.
+ * kernel_cache may be NULL only when M_max == 0.  Device errors (n_path outside
+ * [0, n_draft], kv_len below it or past L_max, a path entry that is no draft, a
+ * completed kernel past M_max) set the error word; that sequence is skipped.
+ * Other cache rows and kernels are untouched.
+ */
+int infllmv2_commit(const void* draft_k, const void* draft_v, const int32_t* path, const int32_t* n_path, void* k_cache,
+                    void* v_cache, void* kernel_cache, const int32_t* kv_len, int B, int n_draft, int Hkv, int d,
+                    int L_max, int M_max, const infllmv2_params* params, void* stream);
+
+/*
  * Allocation-free decode.  The paper has no counterpart: this entry point is
  * for callers of this library that cannot provide a workspace -- a process whose
  * device memory is reserved up front by its own pool, a plugin that receives
@@ -393,7 +559,7 @@ int infllmv2_decode_noalloc(const void* q, const void* k_cache, const void* v_ca
  * those events and writes the elapsed milliseconds of each stage of the most
  * recent call into ms[0 .. *n_stages-1] (at most max_stages), and
  * infllmv2_profile_stage_name(i) names stage i ("pool", "score", "topk",
- * "attend", "combine").  Events live in the library, per device, created on
+ * "attend", "combine", "rope", "verify", "commit").  Events live in the library, per device, created on
  * first use; enabling costs one event record per kernel.  Not thread-safe.
  * Returns INFLLMV2_OK or INFLLMV2_ERR_CUDA.
  */
