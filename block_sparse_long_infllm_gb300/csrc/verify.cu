@@ -18,26 +18,35 @@
 // clock and SM).
 //
 // What bounds it is memory: the last node's target row (and draft row, once a child was rejected).
-// One thread-block cluster per sequence, the row split over its CTAs and warps in contiguous
-// pieces; the CTAs exchange their sums in distributed shared memory, and the warp that holds the
-// sampled token reads its piece again.
-#include <cooperative_groups.h>
-
+// One thread-block cluster per sequence; a row is cut into one contiguous piece per warp.  In each
+// sweep the warps send their pieces' sums to every CTA (asynchronous stores counted on the receiver's
+// barrier: a cluster barrier that also orders plain stores took about 0.9 us instead of 0.25), warp 0
+// of every CTA takes the same decisions from them, and at the end the warp whose piece holds the
+// sampled token finds it from the running sums that its lanes left in shared memory.  Decisions are
+// integer too: 128-bit products compare u Z q with w R exactly.
 #include "internal.h"
+#include "tma.cuh"
 
 namespace infllmv2 {
 
 namespace {
 
-namespace cg = cooperative_groups;
 using u64 = unsigned long long;
 
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kResident = 4;  // CTAs per SM
 constexpr int kMaxCluster = 8;
-constexpr float kMostSum = 2.f;  // a row whose sum is above this holds no probabilities
+constexpr int kMaxPieces = kMaxCluster * kVerifyWarps;  // pieces of a row: one per warp of the cluster
+constexpr int kLanePieces = kMaxPieces / 32;
+constexpr int kBatch = 4;     // chunks of each row that a lane loads together
+constexpr int kSegments = 16; // running sums of a piece that its lanes leave for the search
+constexpr u64 kOne = 1ull << 62;  // probability 1 in the units of the sums
+constexpr float kMostSum = 2.f;   // a row whose sum is above this holds no probabilities
 
-// Shift right by any amount (63 and more leave 0; PTX clamps the amount).
+// ---- 64-bit numbers
+
+// Shift right by any amount (PTX clamps it: 64 and more leave 0).
 __device__ __forceinline__ u64 shr(u64 x, int n) {
     u64 y;
     asm("shr.u64 %0, %1, %2;" : "=l"(y) : "l"(x), "r"(n));
@@ -47,193 +56,353 @@ __device__ __forceinline__ u64 shr(u64 x, int n) {
 // A probability as read: NaN and negative values are 0, values past 1 are 1.
 __device__ __forceinline__ float prob(float x) { return __saturatef(x); }
 
-// p in [0, 1] in units of 2^-62, bits below that dropped.
-__device__ __forceinline__ u64 fixed(float p) {
-    const uint32_t b = __float_as_uint(p);
-    return shr(static_cast<u64>(((b & 0x7FFFFFu) | 0x800000u) << 7) << 32, 127 - static_cast<int>(b >> 23));
+// acc + p in units of 2^-62, p in [0, 1], bits below that dropped: the mantissa (leading bit at 31)
+// times 2^(exponent - 96), or shifted right where that is negative -- one 64-bit multiply-add.
+__device__ __forceinline__ u64 add_fixed(u64 acc, float p) {
+    const uint32_t b = __float_as_uint(p), m = (b << 8) | 0x80000000u;
+    const int e = static_cast<int>(b >> 23) - 96;
+    return acc + static_cast<u64>(__funnelshift_rc(m, 0u, max(-e, 0))) * (1u << max(e, 0));
 }
 
-// c as a 64-bit mantissa with its leading bit set and an exponent: c = m 2^(e - 63).
-struct Coef {
+// A positive number m 2^(e - 63), the leading bit of m set.
+struct Num {
     u64 m;
     int e;
+};
+// x in units of 2^-62 (x != 0).
+__device__ __forceinline__ Num num(u64 x) {
+    const int z = __clzll(static_cast<long long>(x));
+    return Num{x << z, 1 - z};
+}
+__device__ __forceinline__ Num add(Num a, Num b) {
+    if (a.e < b.e) {
+        const Num t = a;
+        a = b;
+        b = t;
+    }
+    Num r{a.m + shr(b.m, a.e - b.e), a.e};
+    if (r.m < a.m) {
+        r.m = (r.m >> 1) | (1ull << 63);
+        ++r.e;
+    }
+    return r;
+}
+// a / b: two Newton steps from an fp32 reciprocal, y -> y + y (1 - b y), y 2^-62 the reciprocal of b's
+// mantissa in [1, 2): 2^-23, 2^-46, then the arithmetic's 2^-60.
+__device__ __forceinline__ Num divide(Num a, Num b) {
+    u64 y = static_cast<u64>(__fdiv_rn(0x1p62f, __ull2float_rn(b.m) * 0x1p-63f));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const long long err = static_cast<long long>((1ull << 61) - __umul64hi(b.m, y));  // (1 - b y) 2^61
+        y += static_cast<u64>(__mul64hi(static_cast<long long>(y), err) * 8);
+    }
+    const u64 q = __umul64hi(a.m, y);  // quotient of the mantissas in (1/2, 2), times 2^61
+    const int z = __clzll(static_cast<long long>(q));
+    return Num{q << z, a.e - b.e + 2 - z};
+}
+
+// c, the factor of the draft's row in w.
+struct Coef {
+    Num v;
     int kind;  // 0: c = 0, 1: c = 1, 2: any other
 };
-__device__ __forceinline__ Coef coef(double c) {
-    const u64 b = static_cast<u64>(__double_as_longlong(c));
-    Coef r;
-    r.m = ((b & 0xFFFFFFFFFFFFFull) | 0x10000000000000ull) << 11;
-    r.e = static_cast<int>(b >> 52) - 1023;
-    r.kind = c == 0.0 ? 0 : c == 1.0 ? 1 : 2;
-    return r;
+
+// c q in units of 2^-62; all ones where it is 2 or more (past any p).
+__device__ __forceinline__ u64 scaled(float q, const Num& c) {
+    const uint32_t b = __float_as_uint(q);
+    const int e = c.e + static_cast<int>(b >> 23) - 127;
+    // both mantissas have their leading bit at 63: the product's high word is c q 2^(62 - e)
+    const u64 h = __umul64hi(c.m, static_cast<u64>((b << 8) | 0x80000000u) << 32);
+    return b == 0u ? 0ull : e > 0 ? ~0ull : shr(h, -e);
 }
 
 // w = max(p - c q, 0) in units of 2^-62.
-template <int KIND>
 __device__ __forceinline__ u64 weight(float p, float q, const Coef& c) {
-    const u64 P = fixed(p);
-    if constexpr (KIND == 0) return P;
-    u64 Q;
-    if constexpr (KIND == 1) {
-        Q = fixed(q);
-    } else {
-        const uint32_t b = __float_as_uint(q);
-        const int e = c.e + static_cast<int>(b >> 23) - 127;
-        // both mantissas have their leading bit at 63: the product's high word is c q 2^(62 - e)
-        const u64 h = __umul64hi(c.m, static_cast<u64>((b << 8) | 0x80000000u) << 32);
-        Q = e > 0 ? ~0ull : shr(h, -e);  // e > 0: c q is at least 2, past any p
-        if (b == 0u) Q = 0ull;
-    }
+    const u64 P = add_fixed(0ull, p);
+    const u64 Q = c.kind == 0 ? 0ull : c.kind == 1 ? add_fixed(0ull, q) : scaled(q, c.v);
     return P > Q ? P - Q : 0ull;
 }
 
+// u Z q < w R, exactly: u, q in [0, 1]; Z, w, R in units of 2^-62.  The 128-bit products are compared
+// after the left one is cut to whole units of the right one (x < n iff floor(x) < n).
+__device__ __forceinline__ bool stands(float u, u64 Z, float q, u64 w, u64 R) {
+    const uint32_t ub = __float_as_uint(u), qb = __float_as_uint(q);
+    const u64 uq = static_cast<u64>((ub << 8) | 0x80000000u) * ((qb << 8) | 0x80000000u);
+    const int s = 254 - static_cast<int>(ub >> 23) - static_cast<int>(qb >> 23);  // u q = uq 2^(-62 - s)
+    u64 lo = uq * Z, hi = __umul64hi(uq, Z);
+    if (s >= 64) {
+        lo = shr(hi, s - 64);
+        hi = 0ull;
+    } else if (s > 0) {
+        lo = (lo >> s) | (hi << (64 - s));
+        hi >>= s;
+    }
+    const u64 rh = __umul64hi(w, R), rl = w * R;
+    return hi < rh || (hi == rh && lo < rl);
+}
+
+// ---- rows
+
+// A row in 16-byte chunks of memory: chunk k holds elements k*N - skew .. of the row, `skew` the row's
+// distance from a 16-byte boundary.
 template <typename T>
-struct Chunk {  // 16 bytes of a row
+struct RowView {
     static constexpr int N = 16 / sizeof(T);
-    float x[N];
+    const T* p;
+    int skew, V;
+    // Chunks [lo, hi) lie wholly inside the row; one at either end may be cut.
+    __device__ __forceinline__ int lo() const { return skew != 0 ? 1 : 0; }
+    __device__ __forceinline__ int hi() const { return (skew + V) / N; }
+    __device__ __forceinline__ int chunks() const { return (skew + V + N - 1) / N; }
+    // Chunk k if `want`, else 0.  One predicated load, so that several in a row are in flight together
+    // (a branch around each load would make them wait for one another).
+    __device__ __forceinline__ uint4 whole(int k, bool want) const {
+        uint4 r = make_uint4(0u, 0u, 0u, 0u);
+        asm("{\n"
+            " .reg .pred p;\n"
+            " setp.ne.s32 p, %5, 0;\n"
+            " @p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+            "}\n"
+            : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w)
+            : "l"(p - skew + static_cast<long long>(k) * N), "r"(want ? 1 : 0));
+        return r;
+    }
+    // A cut chunk, element by element; elements outside the row are 0.
+    __device__ __noinline__ uint4 edge(int k) const {
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int i = k * N - skew + e;
+            if (i < 0 || i >= V) continue;
+            if constexpr (sizeof(T) == 4)
+                w[e] = __float_as_uint(p[i]);
+            else
+                w[e >> 1] |= static_cast<uint32_t>(__bfloat16_as_ushort(p[i])) << (16 * (e & 1));
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
 };
+
+// Element e of a chunk as a probability.
+template <typename T>
+__device__ __forceinline__ float element(const uint4& x, int e) {
+    if constexpr (sizeof(T) == 4) {
+        return prob(__uint_as_float(e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w));
+    } else {
+        const uint32_t w = (e >> 1) == 0 ? x.x : (e >> 1) == 1 ? x.y : (e >> 1) == 2 ? x.z : x.w;
+        return prob((e & 1) ? bf16_hi(w) : bf16_lo(w));
+    }
+}
 
 __device__ __forceinline__ float load1(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-// Elements k*N - a .. of the row (a: the row's distance from a 16-byte boundary), 0 outside it.
-template <typename T>
-__device__ __forceinline__ Chunk<T> load_chunk(const T* row, int k, int a, int V) {
-    constexpr int N = Chunk<T>::N;
-    Chunk<T> r;
-    const int i0 = k * N - a;
-    if (i0 >= 0 && i0 + N <= V) {
-        const uint4 w = ldg_v4_stream(row + i0);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            if constexpr (sizeof(T) == 4) {
-                r.x[e] = prob(__uint_as_float(ws[e]));
-            } else {
-                r.x[e] = prob((e & 1) ? bf16_hi(ws[e >> 1]) : bf16_lo(ws[e >> 1]));
-            }
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) r.x[e] = i0 + e >= 0 && i0 + e < V ? prob(load1(row + i0 + e)) : 0.f;
-    }
-    return r;
-}
-
+// A lane's sums over its chunks: of p, and of what w loses against it.
 struct Sums {
-    u64 w;
-    float p;
+    u64 p = 0ull, q = 0ull;
+    uint32_t top = 0u;  // bit 31: the sum of p reached 2 (before it could wrap)
+
+    // w = max(p - c q, 0) = p - min(p, c q)
+    template <typename T, int KIND>
+    __device__ __forceinline__ void take(const uint4& P, const uint4& Q, const Num& c) {
+#pragma unroll
+        for (int e = 0; e < 16 / static_cast<int>(sizeof(T)); ++e) {
+            const float x = element<T>(P, e);
+            if constexpr (KIND == 2) {
+                const u64 px = add_fixed(0ull, x), y = scaled(element<T>(Q, e), c);
+                p += px;
+                q += px < y ? px : y;
+            } else {
+                p = add_fixed(p, x);
+                if constexpr (KIND == 1) q = add_fixed(q, fminf(x, element<T>(Q, e)));
+            }
+            if (e & 1) top |= static_cast<uint32_t>(p >> 32);
+        }
+    }
+    __device__ __forceinline__ float about() const {  // the sum of p
+        return (top >> 31) != 0u ? 4.f : __uint2float_rn(static_cast<uint32_t>(p >> 32)) * 0x1p-30f;
+    }
 };
 
-// Sum of w and of p over chunks [k0, k1), for this lane.
-template <typename T, int KIND>
-__device__ __forceinline__ Sums sweep(const T* p, const T* q, int k0, int k1, int a, int V, const Coef& c) {
-    constexpr int N = Chunk<T>::N;
-    Sums s{0ull, 0.f};
-#pragma unroll 4
-    for (int k = k0 + (threadIdx.x & 31); k < k1; k += 32) {
-        const Chunk<T> P = load_chunk(p, k, a, V);
-        Chunk<T> Q = P;
-        if constexpr (KIND != 0) Q = load_chunk(q, k, a, V);
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            s.w += weight<KIND>(P.x[e], Q.x[e], c);
-            s.p += P.x[e];
-        }
-    }
-    return s;
-}
+struct Part {  // one piece's sums
+    u64 w;
+    float p;
+    float pad;
+};
 
 struct Shared {
+    alignas(16) Part part[2][kMaxPieces];
+    alignas(8) uint64_t bar[2];  // bytes of part[.] that came from the cluster's warps
     int tok[64];
     u64 mask[64];
     float u[64];
     float p[64], q[64];  // of each node's token in its parent's rows
     u64 kids[64];
-    u64 warp_w[kVerifyWarps];
-    float warp_p[kVerifyWarps];
-    u64 part_w[2][kMaxCluster];
-    float part_p[2][kMaxCluster];
-    // the next sweep
-    double c;
-    int node;
-    int last;   // it draws the final token
-    u64 gone;   // children of `node` whose tokens are out (drafts without probabilities)
-    u64 on;     // the path so far
+    u64 stands;          // nodes that stand if they are tried first
+    u64 cum[kSegments][kVerifyThreads];  // each lane's sum of w up to the end of a segment of its piece
+    // what warp 0 tells the others: the next sweep, then where the last token is
+    Coef c;
+    u64 gone;            // children of `node` whose tokens weigh nothing (drafts without probabilities)
+    u64 on;              // the path
+    u64 rem;             // what is left of the target in piece `own`
+    int node, own, state;
 };
+enum : int { kSweep = 0, kDraw = 1, kDone = 2, kBad = 3 };
 
-// The first element of chunks [k0, k1) whose running sum of w passes T (T below their sum), by one warp.
-template <typename T, int KIND>
-__device__ int search(const T* p, const T* q, int k0, int k1, int a, int V, const Coef& c, u64 target, u64 gone,
-                      const int* tok) {
-    constexpr int N = Chunk<T>::N;
+__device__ __forceinline__ u64 warp_sum(u64 x) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+}
+__device__ __forceinline__ u64 warp_scan(u64 x) {  // inclusive
     const int lane = threadIdx.x & 31;
-    u64 base = 0ull;
-    for (int kb = k0; kb < k1; kb += 32) {
-        const int k = kb + lane;
-        u64 w[N], sum = 0ull;
-        if (k < k1) {
-            const Chunk<T> P = load_chunk(p, k, a, V);
-            Chunk<T> Q = P;
-            if constexpr (KIND != 0) Q = load_chunk(q, k, a, V);
 #pragma unroll
-            for (int e = 0; e < N; ++e) w[e] = weight<KIND>(P.x[e], Q.x[e], c);
-            for (u64 g = gone; g != 0ull; g &= g - 1) {
-                const int at = tok[__ffsll(static_cast<long long>(g)) - 1] - (k * N - a);
+    for (int off = 1; off < 32; off <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+    }
+    return x;
+}
+
+__device__ __forceinline__ uint32_t peer_addr(uint32_t local, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+    return r;
+}
+// 16 bytes into a peer's shared memory, counted on the peer's barrier.
+__device__ __forceinline__ void send16(uint32_t dst, u64 a, u64 b, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(dst), "l"(a),
+                 "l"(b), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ int lowest(u64 x) { return __ffsll(static_cast<long long>(x)) - 1; }
+
+// One row's weights, as a search reads them.
+template <typename T>
+struct Weights {
+    static constexpr int N = RowView<T>::N;
+    RowView<T> P, Q;
+    Coef c;
+    u64 out;         // children whose tokens weigh nothing (drafts without probabilities)
+    const int* tok;
+
+    __device__ __forceinline__ void chunk(int k, int k1, u64 (&w)[N]) const {
 #pragma unroll
-                for (int e = 0; e < N; ++e)
-                    if (e == at) w[e] = 0ull;
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < N; ++e) w[e] = 0ull;
+        for (int e = 0; e < N; ++e) w[e] = 0ull;
+        const bool in = k >= P.lo() && k < min(k1, P.hi());
+        uint4 x = P.whole(k, in), y = Q.whole(k, in && c.kind != 0);
+        if (k < k1 && !in) {
+            x = P.edge(k);
+            if (c.kind != 0) y = Q.edge(k);
         }
 #pragma unroll
-        for (int e = 0; e < N; ++e) sum += w[e];
-        u64 incl = sum;
+        for (int e = 0; e < N; ++e) w[e] = weight(element<T>(x, e), element<T>(y, e), c);
+        for (u64 g = out; g != 0ull; g &= g - 1) {
+            const int at = tok[lowest(g)] - (k * N - P.skew);
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const u64 y = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += y;
+            for (int e = 0; e < N; ++e)
+                if (e == at) w[e] = 0ull;
         }
-        const uint32_t hit = __ballot_sync(0xffffffffu, base + incl > target);
-        if (hit != 0u) {
-            int found = -1;
-            if (lane == __ffs(hit) - 1) {
-                u64 run = base + incl - sum;
+    }
+
+    // The first element of chunks [k0, k1) whose running sum passes `target` (below their sum), by one
+    // warp; every lane returns it.
+    __device__ __noinline__ int search(int k0, int k1, u64 target) const {
+        const int lane = threadIdx.x & 31;
+        u64 base = 0ull;
+        for (int kb = k0; kb < k1; kb += 32) {
+            u64 w[N], sum = 0ull;
+            chunk(kb + lane, k1, w);
+#pragma unroll
+            for (int e = 0; e < N; ++e) sum += w[e];
+            const u64 incl = base + warp_scan(sum);
+            const uint32_t hit = __ballot_sync(0xffffffffu, incl > target);
+            if (hit != 0u) {
+                int found = -1;
+                u64 run = incl - sum;
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
                     run += w[e];
-                    if (found < 0 && run > target) found = k * N - a + e;
+                    if (found < 0 && run > target) found = (kb + lane) * N - P.skew + e;
                 }
+                return __shfl_sync(0xffffffffu, found, __ffs(hit) - 1);
             }
-            return __shfl_sync(0xffffffffu, found, __ffs(hit) - 1);
+            base = __shfl_sync(0xffffffffu, incl, 31);
         }
-        base += __shfl_sync(0xffffffffu, incl, 31);
+        return -1;
     }
-    return -1;
+};
+
+// A warp's sums over its piece, chunks [k0, k1) in `its` rounds of 32; each lane leaves its running sum
+// behind every `seg` rounds.
+template <typename T, int KIND>
+__device__ __forceinline__ Sums sweep(const RowView<T>& P, const RowView<T>& Q, const Num& c, int k0, int k1, int its,
+                                      int seg, u64 (*cum)[kVerifyThreads]) {
+    const int lane = threadIdx.x & 31, lo = max(P.lo(), k0), hi = min(P.hi(), k1);
+    Sums s;
+    if (k0 == 0 && lo > 0 && lane == 0 && k1 > 0) {  // the row's cut first chunk
+        const uint4 x = P.edge(0);
+        s.template take<T, KIND>(x, KIND != 0 ? Q.edge(0) : x, c);
+    }
+    for (int it = 0; it < its; it += kBatch) {
+        uint4 x[kBatch], y[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int k = k0 + 32 * (it + i) + lane;
+            x[i] = P.whole(k, k >= lo && k < hi);
+            if (KIND != 0) y[i] = Q.whole(k, k >= lo && k < hi);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            s.template take<T, KIND>(x[i], KIND != 0 ? y[i] : x[i], c);
+            if (it + i < its && (seg == 1 || (it + i + 1) % seg == 0 || it + i + 1 == its))
+                cum[(it + i) / seg][threadIdx.x] = s.p - s.q;
+        }
+    }
+    const int last = P.chunks() - 1;
+    if (last >= P.hi() && last >= k0 && last < k1 && last >= P.lo() && (last - k0) % 32 == lane) {  // and last one
+        const u64 before = s.p - s.q;
+        const uint4 x = P.edge(last);
+        s.template take<T, KIND>(x, KIND != 0 ? Q.edge(last) : x, c);
+        for (int i = (last - k0) / 32 / seg; i <= (its - 1) / seg; ++i) cum[i][threadIdx.x] += s.p - s.q - before;
+    }
+    return s;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(VerifyArgs a) {
-    constexpr int N = Chunk<T>::N;
+__global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(VerifyArgs a, int CL) {
+    constexpr int N = RowView<T>::N;
     __shared__ Shared sh;
-    cg::cluster_group cluster = cg::this_cluster();
-    const int CL = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
-    const int b = blockIdx.x / CL, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = blockIdx.x % CL, b = blockIdx.x / CL;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int pieces = CL * kVerifyWarps, piece = rank * kVerifyWarps + warp;
     const size_t at = static_cast<size_t>(b) * a.n;
     const T* target = static_cast<const T*>(a.target) + at * a.V;
     const T* draft = a.draft != nullptr ? static_cast<const T*>(a.draft) + at * a.V : nullptr;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.bar[i], 1);
+            mbar_arrive_expect_tx(&sh.bar[i], pieces * sizeof(Part));
+        }
+        fence_mbar_init();
+        sh.stands = 0ull;
+    }
+    if (tid < 64) sh.kids[tid] = 0ull;
     const int n = a.n_nodes != nullptr ? a.n_nodes[b] : a.n;
     bool bad = n < 0 || n > a.n;
-    if (tid < 64) sh.kids[tid] = 0ull;
-    if (!bad && tid < n) {
+    if (tid < a.n) {
         sh.tok[tid] = a.tokens[at + tid];
         sh.u[tid] = __saturatef(a.u[at + tid]);
         const u64 own = 1ull << tid;
         sh.mask[tid] = a.tree_mask != nullptr ? a.tree_mask[at + tid] : own | (own - 1);
     }
     __syncthreads();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA's barriers are there
     if (!bad && tid < n) {
         const u64 own = 1ull << tid, up = sh.mask[tid] ^ own;
         if (tid == 0) {
@@ -245,179 +414,204 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(VerifyArgs a) {
             if (!bad) {
                 atomicOr(&sh.kids[parent], own);
                 const size_t i = static_cast<size_t>(parent) * a.V + x;
-                sh.p[tid] = prob(load1(target + i));
-                sh.q[tid] = draft != nullptr ? prob(load1(draft + i)) : 1.f;
+                const float p = prob(load1(target + i)), q = draft != nullptr ? prob(load1(draft + i)) : 1.f;
+                sh.p[tid] = p;
+                sh.q[tid] = q;
+                if (stands(sh.u[tid], kOne, q, add_fixed(0ull, p), kOne)) atomicOr(&sh.stands, own);
             }
         }
     }
     bad = __syncthreads_or(bad) != 0;
-    if (n <= 0) bad = true;
-    // thread 0's walk
-    int cur = 0, drawn = -1;
-    u64 rest = bad ? 0ull : sh.kids[0];
-    u64 gone = 0ull, on = 1ull;
-    double c = 0.0, Z = 1.0, R = 1.0;
-    bool z_known = true;
-    if (!bad) {
-        cluster.sync();  // every CTA of the cluster runs before any writes into another
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const bool idle = n <= 0 || bad;
+    int drawn = -1;
+    if (!idle) {
+        // the walk (warp 0)
+        u64 on = 1ull, rest = sh.kids[0], gone = 0ull, Z = kOne;
+        long long R = static_cast<long long>(kOne);
+        Coef c{{0ull, 0}, 0};
+        int cur = 0;
+        bool fresh = true, z_known = true;  // no child of cur was tried yet; Z belongs to c
         for (int round = 0;; ++round) {
-            if (tid == 0) {
-                while (rest != 0ull) {
-                    const int i = __ffsll(static_cast<long long>(rest)) - 1;
-                    const double p = sh.p[i], q = sh.q[i], u = sh.u[i];
-                    double w;
-                    if (draft != nullptr) {
-                        if (!z_known) break;
-                        w = fmax(p - c * q, 0.0);
+            if (warp == 0) {
+                while (rest != 0ull && z_known) {
+                    const int i = lowest(rest);
+                    const float q = sh.q[i];
+                    u64 w = 0ull;
+                    bool stand;
+                    if (fresh && draft != nullptr) {
+                        stand = ((sh.stands >> i) & 1ull) != 0ull;
                     } else {
-                        w = p;
+                        w = weight(sh.p[i], q, c);  // c = 0 without draft probabilities
                         for (u64 g = gone; g != 0ull; g &= g - 1)
-                            if (sh.tok[__ffsll(static_cast<long long>(g)) - 1] == sh.tok[i]) w = 0.0;
+                            if (sh.tok[lowest(g)] == sh.tok[i]) w = 0ull;
+                        stand = R > 0 && stands(sh.u[i], Z, q, w, static_cast<u64>(R));
                     }
-                    if (u * Z * q < w * R) {
+                    if (stand) {
                         cur = i;
                         on |= 1ull << i;
                         rest = sh.kids[i];
                         gone = 0ull;
-                        c = 0.0;
-                        Z = R = 1.0;
-                        z_known = true;
+                        c.kind = 0;
+                        Z = kOne;
+                        R = static_cast<long long>(kOne);
+                        fresh = true;
                         continue;
                     }
                     rest &= rest - 1;
+                    fresh = false;
                     if (draft == nullptr) {
                         gone |= 1ull << i;
-                        Z = fmax(Z - w, 0.0);
+                        Z = Z > w ? Z - w : 0ull;
                     } else {
-                        if (R > 0.0) {
-                            c += Z / R;
+                        if (R > 0 && Z != 0ull) {
+                            Num z = num(Z);
+                            if (R != static_cast<long long>(kOne)) z = divide(z, num(static_cast<u64>(R)));
+                            c.v = c.kind == 0 ? z : add(c.v, z);
+                            c.kind = c.v.m == (1ull << 63) && c.v.e == 0 ? 1 : 2;
                             z_known = false;
                         }
-                        if (!a.replace) R -= q;
+                        if (!a.replace) R -= static_cast<long long>(add_fixed(0ull, q));
                     }
-                }
-                sh.c = c;
-                sh.node = cur;
-                sh.last = rest == 0ull;
-                sh.gone = gone;
-                sh.on = on;
-            }
-            __syncthreads();
-            const int node = sh.node, fin = sh.last;
-            Coef cf = coef(sh.c);
-            u64 out = sh.gone;
-            const T* p = target + static_cast<size_t>(node) * a.V;
-            const T* q = draft + (draft != nullptr ? static_cast<size_t>(node) * a.V : 0);
-            // the row in 16-byte chunks of memory, contiguous ones for each warp of the cluster
-            const int skew = static_cast<int>(((at + node) * a.V) % N);
-            const int chunks = (skew + a.V + N - 1) / N;
-            const int per_warp = (chunks + CL * kVerifyWarps - 1) / (CL * kVerifyWarps);
-            const int k0 = min((rank * kVerifyWarps + warp) * per_warp, chunks), k1 = min(k0 + per_warp, chunks);
-            u64 whole = 0ull, mine = 0ull, before = 0ull;
-            float sum_p = 0.f;
-            for (int again = 0;; ++again) {  // once, and once more where nothing is left to draw from
-                Sums s = cf.kind == 0   ? sweep<T, 0>(p, q, k0, k1, skew, a.V, cf)
-                         : cf.kind == 1 ? sweep<T, 1>(p, q, k0, k1, skew, a.V, cf)
-                                        : sweep<T, 2>(p, q, k0, k1, skew, a.V, cf);
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) {
-                    s.w += __shfl_xor_sync(0xffffffffu, s.w, off);
-                    s.p += __shfl_xor_sync(0xffffffffu, s.p, off);
                 }
                 if (lane == 0) {
-                    sh.warp_w[warp] = s.w;
-                    sh.warp_p[warp] = s.p;
+                    sh.c = c;
+                    sh.gone = gone;
+                    sh.on = on;
+                    sh.node = cur;
                 }
-                __syncthreads();
-                if (tid < 64 && ((out >> tid) & 1ull) != 0ull) {  // rejected tokens leave their warp's sum, once each
+            }
+            __syncthreads();
+            const Coef cf = sh.c;
+            const u64 out = sh.gone;
+            const int node = sh.node;
+            const int skew = static_cast<int>(((at + node) * a.V) % N);
+            const RowView<T> P{target + static_cast<size_t>(node) * a.V, skew, a.V};
+            const RowView<T> Q{draft + (draft != nullptr ? static_cast<size_t>(node) * a.V : 0), skew, a.V};
+            const int per_piece = (P.chunks() + pieces - 1) / pieces, its = (per_piece + 31) / 32;
+            const int seg = (its + kSegments - 1) / kSegments;
+            const int k0 = min(piece * per_piece, P.chunks()), k1 = min(k0 + per_piece, P.chunks());
+            const Sums s = cf.kind == 0   ? sweep<T, 0>(P, Q, cf.v, k0, k1, its, seg, sh.cum)
+                           : cf.kind == 1 ? sweep<T, 1>(P, Q, cf.v, k0, k1, its, seg, sh.cum)
+                                          : sweep<T, 2>(P, Q, cf.v, k0, k1, its, seg, sh.cum);
+            u64 sw = warp_sum(s.p - s.q);
+            const float sp = warp_sum(s.about());
+            for (u64 g = out; g != 0ull; g &= g - 1) {  // rejected tokens leave their piece's sum, once each
+                const int i = lowest(g), x = sh.tok[i];
+                bool first = true;
+                for (u64 f = out & ((1ull << i) - 1); f != 0ull; f &= f - 1) first = first && sh.tok[lowest(f)] != x;
+                const int k = (x + skew) / N;
+                if (first && k >= k0 && k < k1) sw -= add_fixed(0ull, sh.p[i]);
+            }
+            const int buf = round & 1;
+            if (lane < CL)
+                send16(peer_addr(smem_u32(&sh.part[buf][piece]), lane), sw, __float_as_uint(sp),
+                       peer_addr(smem_u32(&sh.bar[buf]), lane));
+            if (warp == 0) {
+                int state = kSweep, own = -1;
+                u64 rem = 0ull;
+                if (!mbar_wait(&sh.bar[buf], (round >> 1) & 1)) {
+                    if (lane == 0) raise_error(a.err, kDevErrTimeout);
+                    state = kBad;
+                } else {
+                    if (lane == 0) mbar_arrive_expect_tx(&sh.bar[buf], pieces * sizeof(Part));  // the round after the next
+                    // a lane sums its pieces; a scan over the lanes orders them
+                    u64 wl[kLanePieces], sum = 0ull;
+                    float all = 0.f;
+#pragma unroll
+                    for (int i = 0; i < kLanePieces; ++i) {
+                        const int e = lane * kLanePieces + i;
+                        wl[i] = e < pieces ? sh.part[buf][e].w : 0ull;
+                        all += e < pieces ? sh.part[buf][e].p : 0.f;
+                        sum += wl[i];
+                    }
+                    all = warp_sum(all);
+                    const u64 incl = warp_scan(sum), whole = __shfl_sync(0xffffffffu, incl, 31);
+                    if (!(all <= kMostSum)) {
+                        state = kBad;
+                    } else if (rest != 0ull) {
+                        Z = whole;
+                        z_known = true;
+                    } else if (whole == 0ull) {  // nothing of p is left: draw from p itself
+                        if (c.kind == 0 && gone == 0ull) state = kBad;
+                        c.kind = 0;
+                        gone = 0ull;
+                    } else {
+                        state = kDraw;
+                        // floor(u whole): u = m 2^(exponent - 126) / 2^32, m with its leading bit at 31
+                        const uint32_t ub = __float_as_uint(sh.u[0]);
+                        u64 T0 = shr(__umul64hi(whole, static_cast<u64>((ub << 8) | 0x80000000u) << 32),
+                                     126 - static_cast<int>(ub >> 23));
+                        if (ub >= 0x3F800000u) T0 = whole - 1;  // u = 1: the last token with any weight
+                        // the piece that holds it, and how far into it
+                        const int hit = __ffs(__ballot_sync(0xffffffffu, incl > T0)) - 1;
+                        rem = T0 - (incl - sum);
+#pragma unroll
+                        for (int i = 0; i < kLanePieces; ++i) {
+                            if (own < 0 && rem < wl[i]) own = lane * kLanePieces + i;
+                            if (own < 0) rem -= wl[i];
+                        }
+                        own = __shfl_sync(0xffffffffu, own, hit);
+                        rem = __shfl_sync(0xffffffffu, rem, hit);
+                    }
+                }
+                if (lane == 0) {
+                    sh.state = state;
+                    sh.own = own;
+                    sh.rem = rem;
+                }
+            }
+            __syncthreads();
+            const int state = sh.state;
+            if (state == kSweep) continue;
+            bad = state == kBad;
+            if (!bad && sh.own == piece) {
+                // the segment (lane i sums the piece's i-th), then the token in it
+                u64 rem = sh.rem, tot = 0ull;
+                const int segs = (its - 1) / seg + 1;
+                if (lane < segs)
+                    for (int i = 0; i < 32; ++i) tot += sh.cum[lane][warp * 32 + ((i + lane) & 31)];
+                for (u64 g = out; g != 0ull; g &= g - 1) {
+                    const int i = lowest(g), x = sh.tok[i];
                     bool first = true;
-                    for (u64 g = out & ((1ull << tid) - 1); g != 0ull; g &= g - 1)
-                        if (sh.tok[__ffsll(static_cast<long long>(g)) - 1] == sh.tok[tid]) first = false;
-                    const int owner = (sh.tok[tid] + skew) / N / per_warp;
-                    if (first && owner / kVerifyWarps == rank)
-                        atomicAdd(&sh.warp_w[owner % kVerifyWarps], 0ull - fixed(sh.p[tid]));
+                    for (u64 f = out & ((1ull << i) - 1); f != 0ull; f &= f - 1) first = first && sh.tok[lowest(f)] != x;
+                    const int k = (x + skew) / N;
+                    if (first && k >= k0 && k < k1 && lane >= (k - k0) / 32 / seg) tot -= add_fixed(0ull, sh.p[i]);
                 }
-                __syncthreads();
-                const int buf = (round + again) & 1;
-                if (tid < CL) {
-                    u64 w = 0ull;
-                    float pp = 0.f;
-                    for (int i = 0; i < kVerifyWarps; ++i) {
-                        w += sh.warp_w[i];
-                        pp += sh.warp_p[i];
-                    }
-                    Shared* peer = cluster.map_shared_rank(&sh, tid);
-                    peer->part_w[buf][rank] = w;
-                    peer->part_p[buf][rank] = pp;
-                }
-                cluster.sync();
-                whole = before = 0ull;
-                sum_p = 0.f;
-                for (int i = 0; i < CL; ++i) {
-                    if (i < rank) before += sh.part_w[buf][i];
-                    whole += sh.part_w[buf][i];
-                    sum_p += sh.part_p[buf][i];
-                }
-                mine = sh.part_w[buf][rank];
-                if (!fin || whole != 0ull || (cf.kind == 0 && out == 0ull)) {
-                    round += again;
-                    break;
-                }
-                cf = coef(0.0);  // nothing of p is left: draw from p itself
-                out = 0ull;
+                const int which = __ffs(__ballot_sync(0xffffffffu, lane < segs && tot > rem)) - 1;
+                const u64 prev = __shfl_sync(0xffffffffu, tot, max(which - 1, 0));
+                if (which > 0) rem -= prev;
+                const int s0 = k0 + 32 * seg * which;
+                drawn = Weights<T>{P, Q, cf, out, sh.tok}.search(s0, min(s0 + 32 * seg, k1), rem);
             }
-            if (!(sum_p <= kMostSum) || (fin && whole == 0ull)) {
-                bad = true;
-                break;
-            }
-            if (fin) {
-                // floor(u whole): u = m 2^-(150 - exponent), m of 24 bits
-                const uint32_t ub = __float_as_uint(sh.u[0]);
-                u64 T0 = shr(__umul64hi(whole, static_cast<u64>((ub << 8) | 0x80000000u) << 32),
-                             126 - static_cast<int>(ub >> 23));
-                if (ub >= 0x3F800000u) T0 = whole - 1;  // u = 1: the last token with any weight
-                if (T0 >= before && T0 - before < mine) {
-                    u64 rem = T0 - before;
-                    int w = 0;
-                    while (w < kVerifyWarps - 1 && rem >= sh.warp_w[w]) rem -= sh.warp_w[w++];
-                    if (warp == w) {
-                        drawn = cf.kind == 0   ? search<T, 0>(p, q, k0, k1, skew, a.V, cf, rem, out, sh.tok)
-                                : cf.kind == 1 ? search<T, 1>(p, q, k0, k1, skew, a.V, cf, rem, out, sh.tok)
-                                               : search<T, 2>(p, q, k0, k1, skew, a.V, cf, rem, out, sh.tok);
-                    }
-                }
-                break;
-            }
-            Z = static_cast<double>(whole) * 0x1p-62;
-            z_known = true;
+            break;
         }
     }
-    const u64 path = bad ? 0ull : sh.on;
+    const u64 path = idle || bad ? 0ull : sh.on;
     const int count = __popcll(path);
-    if (rank == 0) {
-        if (bad && n != 0 && tid == 0) raise_error(a.err, kDevErrIndex);
-        if (tid < a.n) {
-            a.path[at + tid] = -1;
-            if (tid != count - 1) a.out_tokens[at + tid] = -1;
-        }
-        if (tid == 0) {
-            a.n_path[b] = count;
-            if (a.kv_len_out != nullptr) a.kv_len_out[b] = a.kv_len[b] + count;
-        }
-        __syncthreads();
-        if (tid < 64 && ((path >> tid) & 1ull) != 0ull) {
+    if (rank == 0 && tid < a.n) {
+        if (tid == 0 && (bad || n < 0)) raise_error(a.err, kDevErrIndex);
+        if (((path >> tid) & 1ull) != 0ull) {
             const int t = __popcll(path & ((1ull << tid) - 1));
             a.path[at + t] = tid;
             if (t > 0) a.out_tokens[at + t - 1] = sh.tok[tid];
+        }
+        if (tid >= count) a.path[at + tid] = a.out_tokens[at + tid] = -1;
+        if (tid == 0) {
+            a.n_path[b] = count;
+            if (a.kv_len_out != nullptr) a.kv_len_out[b] = a.kv_len[b] + count;
         }
     }
     if (drawn >= 0 && lane == 0) a.out_tokens[at + count - 1] = drawn;
 }
 
+// The row of each of B sequences goes to the largest cluster whose CTAs are all resident at once and
+// whose warps each have at least 32 chunks.
 template <typename T>
 cudaError_t launch(const VerifyArgs& a) {
-    int CL = 1;
-    while (CL < kMaxCluster && a.V >= CL * 2 * kVerifyThreads * Chunk<T>::N) CL *= 2;
+    int CL = kMaxCluster;
+    while (CL > 1 && (static_cast<long long>(a.B) * CL > kResident * 152 || a.V < CL * kVerifyThreads * RowView<T>::N))
+        CL /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.B) * CL);
     cfg.blockDim = dim3(kVerifyThreads);
@@ -428,7 +622,7 @@ cudaError_t launch(const VerifyArgs& a) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, verify_kernel<T>, a);
+    return cudaLaunchKernelEx(&cfg, verify_kernel<T>, a, CL);
 }
 
 }  // namespace
