@@ -1,9 +1,10 @@
-"""Build libinfllmv2.so in-tree with nvcc for sm_103a (GB300).
+"""Build libinfllmv2.so in-tree with nvcc for sm_103a (GB300), and the Python module _binding.
 
 Each translation unit compiles in parallel to `_build/`, then nvcc links the
 shared library next to this file.  The CUDA runtime is linked as a shared
 library so the process shares one runtime (and one set of stream handles)
-with PyTorch.
+with PyTorch.  `_binding.so` (csrc/binding.cpp, the host compiler) is linked to
+that library and to PyTorch's.
 """
 from __future__ import annotations
 
@@ -19,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build", "infllmv2")
 LIB_PATH = os.path.join(HERE, "libinfllmv2.so")
+BINDING_PATH = os.path.join(HERE, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "kernel_pool.cu", "select.cu", "decode.cu", "prefill.cu", "decode_noalloc.cu", "tmap.cu", "prefill_tc.cu", "score_tc.cu", "decode_cluster.cu", "bwd.cu", "bwd_tc.cu", "tree_attn.cu", "rope.cu", "verify.cu"]
 
@@ -38,10 +40,42 @@ def _inputs() -> list[str]:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     return any(os.path.getmtime(f) > t for f in _inputs())
+
+
+def _compile_binding() -> str:
+    """csrc/binding.cpp to an object file, against PyTorch's and Python's headers."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    include = [INCLUDE, os.path.join(root, "include"),
+               os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
+               sysconfig.get_paths()["include"]]
+    obj = os.path.join(BUILD_DIR, "binding.o")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [f"-I{p}" for p in include] + ["-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the host compiler failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str):
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, LIB_PATH, f"-L{lib}", "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", f"-Wl,-rpath,$ORIGIN:{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking _binding.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -63,18 +97,21 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(compile_one, SOURCES))
+        binding_obj = binding.result()
     if verbose or ptxas_info:
         for _, log in results:
             if log:
                 sys.stderr.write(log)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + [o for o, _ in results]
+    cmd = [nvcc] + ARCH + ["-shared", "-cudart", "shared", "-Xlinker", "-soname=" + os.path.basename(LIB_PATH), "-o", tmp] + [o for o, _ in results]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_binding(binding_obj)
     return LIB_PATH
 
 

@@ -130,7 +130,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
                  "infllmv2_kernel_pool", "infllmv2_append", "infllmv2_block_select", "infllmv2_sparse_attn_fwd",
                  "infllmv2_decode", "infllmv2_decode_step", "infllmv2_kernel_pool_varlen",
                  "infllmv2_block_select_varlen", "infllmv2_sparse_attn_fwd_varlen", "infllmv2_rope_freqs",
-                 "infllmv2_rope", "infllmv2_rope_append", "infllmv2_rope_append_bwd", "infllmv2_rope_drafts",
+                  "infllmv2_rope", "infllmv2_rope_append", "infllmv2_rope_append_bwd", "infllmv2_rope_drafts",
                  "infllmv2_verify", "infllmv2_commit"):
         getattr(lib, name).restype = ctypes.c_int
     if path == LIB_PATH:
@@ -426,8 +426,6 @@ def decode_noalloc(q, k_cache, v_cache, kernel_cache, kv_len, o, params, lse=Non
 
 # ---- rotary positions, verification of drafts, commit
 
-BF16 = 0  # INFLLMV2_BF16
-FP32 = 1  # INFLLMV2_FP32
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "divisors": 4}  # INFLLMV2_ROPE_*
 
 
@@ -452,177 +450,48 @@ def rope_freqs(rotary_dim: int, base: float = 10000.0, scaling: str = "plain", f
     return freqs, float(scale.value)
 
 
-def _want(name, t, shape, *dtypes):
-    """Type, shape and density of a tensor that a call reads or writes whole."""
-    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {' or '.join(map(str, dtypes))} tensor of shape {tuple(shape)}")
+_native = None
 
 
-def _head_rows(name, t, lead, dtype, d):
-    """[*lead, heads, d] with dense heads and one stride between rows, as a slice of a fused
-    projection has: the heads and the row stride."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype != dtype or len(shape) != len(lead) + 2 or shape[:-2] != lead or shape[-1] != d:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {(*lead, 'heads', d)}")
-    H = shape[-2]
-    width = H * d
-    ok = stride[-1] == 1 and (H == 1 or stride[-2] == d)
-    if len(lead) == 1:
-        ld = stride[0] if lead[0] > 1 else width
-    else:
-        ld = stride[1] if lead[1] > 1 else stride[0] if lead[0] > 1 else width
-        ok = ok and (lead[0] <= 1 or stride[0] == ld * lead[1])
-    if not (ok and ld >= width) and t.numel() > 0:
-        raise ValueError(f"{name} must have dense heads and evenly spaced rows")
-    return H, max(ld, width)
-
-
-def _launch(name, tensors, stream, *args):
-    """Call an entry point on the device of its tensors, on its current stream unless one is given."""
-    import torch
-    dev = None
-    for t in tensors:
-        if t is not None:
-            if dev is None:
-                dev = t.device
-                if dev.type != "cuda":
-                    raise ValueError("tensor must live on a CUDA device")
-            elif t.device != dev:
-                raise ValueError("all tensors must live on one device")
-    if stream is None:
-        s = torch.cuda.current_stream(dev).cuda_stream
-    else:
-        s = stream if isinstance(stream, int) else stream.cuda_stream
-    fn = getattr(load(), name)
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, s)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, s)
-    if rc != OK:
-        raise InfLLMv2Error(rc, name)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _binding():
+    """The module _binding (csrc/binding.cpp): checks of tensors and marshalling of the calls below."""
+    global _native
+    if _native is None:
+        import torch  # noqa: F401  (its libraries are loaded first)
+        load()
+        from . import _binding as module
+        _native = module
+    return _native
 
 
 def rope(q, k, pos, q_out, k_out, freqs, rope, transposed: bool = False, stream=None):
     """Rotary positions of q [rows, Hq, d] and k [rows, Hk, d] (None: q alone), bf16 or fp32, at
     positions pos [rows] int32, to q_out and k_out (which may be q and k).  transposed: the
     gradient of the inputs from that of the outputs.  Rows may be slices of a fused projection."""
-    import torch
-    rows, d = q.shape[0], q.shape[-1]
-    if q.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("q must be bf16 or fp32")
-    if (k is None) != (k_out is None):
-        raise ValueError("k and k_out must be given together")
-    rp = RopeParams.make(rope)
-    lead = (rows,)
-    Hq, ld_q = _head_rows("q", q, lead, q.dtype, d)
-    Hqo, ld_qo = _head_rows("q_out", q_out, lead, q.dtype, d)
-    Hk = Hko = ld_k = ld_ko = 0
-    if k is not None:
-        Hk, ld_k = _head_rows("k", k, lead, q.dtype, d)
-        Hko, ld_ko = _head_rows("k_out", k_out, lead, q.dtype, d)
-    if Hq != Hqo or Hk != Hko:
-        raise ValueError("outputs must have their inputs' heads")
-    _want("pos", pos, lead, torch.int32)
-    _want("freqs", freqs, (rp.rotary_dim // 2,), torch.int64, torch.uint64)
-    _launch("infllmv2_rope", (q, k, pos, q_out, k_out, freqs), stream, q.data_ptr(), ld_q, _addr(k), ld_k,
-            pos.data_ptr(), freqs.data_ptr(), rows, Hq, Hk, d, FP32 if q.dtype == torch.float32 else BF16,
-            1 if transposed else 0, q_out.data_ptr(), ld_qo, _addr(k_out), ld_ko, ctypes.byref(rp))
-
-
-def _chunk(lead, B, cu_q, Tq_max, kv_len, freqs, rp):
-    """Tq and the token rows of a chunk call: rows [B, Tq] without cu_q, [total_q] with it."""
-    import torch
-    _want("kv_len", kv_len, (B,), torch.int32)
-    _want("freqs", freqs, (rp.rotary_dim // 2,), torch.int64, torch.uint64)
-    if cu_q is None:
-        if len(lead) != 2 or lead[0] != B:
-            raise ValueError("rows must be [B, Tq, heads, d] without cu_q")
-        return lead[1], B * lead[1]
-    if len(lead) != 1 or Tq_max is None:
-        raise ValueError("rows must be [total_q, heads, d] with cu_q, and Tq_max be given")
-    _want("cu_q", cu_q, (B + 1,), torch.int32)
-    return int(Tq_max), lead[0]
+    _check(_binding().rope(q, k, pos, q_out, k_out, freqs, rope, transposed, stream), "infllmv2_rope")
 
 
 def rope_append(q, k_new, v_new, q_out, k_cache, v_cache, kv_len, freqs, rope, cu_q=None, Tq_max=None, stream=None):
     """A chunk into the caches: q rotated to q_out, K rotated and V copied into rows kv_len - len .. of
     k_cache, v_cache [B, Hkv, L_max, d].  q, k_new, v_new [B, Tq, heads, d], or packed
     [total_q, heads, d] with cu_q and Tq_max; they may be slices of a fused projection."""
-    import torch
-    bf16 = torch.bfloat16
-    B, Hkv, L_max, d = k_cache.shape
-    rp = RopeParams.make(rope)
-    lead = q.shape[:-2]
-    Tq, total = _chunk(lead, B, cu_q, Tq_max, kv_len, freqs, rp)
-    Hq, ld_q = _head_rows("q", q, lead, bf16, d)
-    Hk, ld_k = _head_rows("k_new", k_new, lead, bf16, d)
-    Hv, ld_v = _head_rows("v_new", v_new, lead, bf16, d)
-    if Hk != Hkv or Hv != Hkv:
-        raise ValueError("k_new and v_new must have the caches' heads")
-    _want("q_out", q_out, q.shape, bf16)
-    _want("k_cache", k_cache, (B, Hkv, L_max, d), bf16)
-    _want("v_cache", v_cache, (B, Hkv, L_max, d), bf16)
-    _launch("infllmv2_rope_append", (q, k_new, v_new, q_out, k_cache, v_cache, kv_len, cu_q, freqs), stream,
-            q.data_ptr(), ld_q, k_new.data_ptr(), ld_k, v_new.data_ptr(), ld_v, q_out.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), kv_len.data_ptr(), _addr(cu_q), freqs.data_ptr(), B, Tq, total, Hq, Hkv, d, L_max,
-            ctypes.byref(rp))
+    _check(_binding().rope_append(q, k_new, v_new, q_out, k_cache, v_cache, kv_len, freqs, rope, cu_q, Tq_max, stream),
+           "infllmv2_rope_append")
 
 
 def rope_append_bwd(dq, dk, dv, dq_out, dk_out, dv_out, kv_len, freqs, rope, cu_q=None, Tq_max=None, stream=None):
     """The gradient of rope_append: from dq (of the rotated q) and dk, dv [B, Hkv, L_max, d] (of the
     caches), fp32 as sparse_attn_bwd gives them, those of the chunk's rows before rotation, bf16 or
     fp32.  The outputs may be slices of a fused gradient; dq_out may be dq."""
-    import torch
-    f32 = torch.float32
-    B, Hkv, L_max, d = dk.shape
-    rp = RopeParams.make(rope)
-    lead = dq.shape[:-2]
-    Tq, total = _chunk(lead, B, cu_q, Tq_max, kv_len, freqs, rp)
-    t = dq_out.dtype
-    if t not in (torch.bfloat16, f32):
-        raise ValueError("dq_out must be bf16 or fp32")
-    Hq, ld_dq = _head_rows("dq_out", dq_out, lead, t, d)
-    Hk, ld_dk = _head_rows("dk_out", dk_out, lead, t, d)
-    Hv, ld_dv = _head_rows("dv_out", dv_out, lead, t, d)
-    if Hk != Hkv or Hv != Hkv:
-        raise ValueError("dk_out and dv_out must have the caches' heads")
-    _want("dq", dq, dq_out.shape, f32)
-    _want("dk", dk, (B, Hkv, L_max, d), f32)
-    _want("dv", dv, (B, Hkv, L_max, d), f32)
-    _launch("infllmv2_rope_append_bwd", (dq, dk, dv, dq_out, dk_out, dv_out, kv_len, cu_q, freqs), stream,
-            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dq_out.data_ptr(), ld_dq, dk_out.data_ptr(), ld_dk,
-            dv_out.data_ptr(), ld_dv, kv_len.data_ptr(), _addr(cu_q), freqs.data_ptr(), B, Tq, total, Hq, Hkv, d, L_max,
-            FP32 if t == f32 else BF16, ctypes.byref(rp))
+    _check(_binding().rope_append_bwd(dq, dk, dv, dq_out, dk_out, dv_out, kv_len, freqs, rope, cu_q, Tq_max, stream),
+           "infllmv2_rope_append_bwd")
 
 
 def rope_drafts(q, k_new, v_new, q_out, draft_k, draft_v, kv_len, tree_mask, freqs, rope, stream=None):
     """A draft tree's rows [B, n_draft, heads, d] as decode takes them: q rotated to q_out, K rotated
     and V copied to draft_k, draft_v [B, Hkv, n_draft, d]; draft i at kv_len + its depth - 1."""
-    import torch
-    bf16 = torch.bfloat16
-    B, Hkv, n, d = draft_k.shape
-    rp = RopeParams.make(rope)
-    lead = (B, n)
-    Hq, ld_q = _head_rows("q", q, lead, bf16, d)
-    Hk, ld_k = _head_rows("k_new", k_new, lead, bf16, d)
-    Hv, ld_v = _head_rows("v_new", v_new, lead, bf16, d)
-    if Hk != Hkv or Hv != Hkv:
-        raise ValueError("k_new and v_new must have the draft buffers' heads")
-    _want("q_out", q_out, q.shape, bf16)
-    _want("draft_k", draft_k, (B, Hkv, n, d), bf16)
-    _want("draft_v", draft_v, (B, Hkv, n, d), bf16)
-    _want("kv_len", kv_len, (B,), torch.int32)
-    _want("tree_mask", tree_mask, lead, torch.int64, torch.uint64)
-    _want("freqs", freqs, (rp.rotary_dim // 2,), torch.int64, torch.uint64)
-    _launch("infllmv2_rope_drafts", (q, k_new, v_new, q_out, draft_k, draft_v, kv_len, tree_mask, freqs), stream,
-            q.data_ptr(), ld_q, k_new.data_ptr(), ld_k, v_new.data_ptr(), ld_v, q_out.data_ptr(), draft_k.data_ptr(),
-            draft_v.data_ptr(), kv_len.data_ptr(), tree_mask.data_ptr(), freqs.data_ptr(), B, n, Hq, Hkv, d,
-            ctypes.byref(rp))
+    _check(_binding().rope_drafts(q, k_new, v_new, q_out, draft_k, draft_v, kv_len, tree_mask, freqs, rope, stream),
+           "infllmv2_rope_drafts")
 
 
 def verify(tokens, target, draft, u, path, n_path, out_tokens, tree_mask=None, n_nodes=None, kv_len=None,
@@ -632,53 +501,12 @@ def verify(tokens, target, draft, u, path, n_path, out_tokens, tree_mask=None, n
     probabilities draft [B, n, V] they were drawn from (None: they were chosen) and the numbers
     u [B, n] in [0, 1).  tree_mask None: a chain.  path, out_tokens [B, n], n_path [B] and, with
     kv_len, kv_len_out [B] (which may be kv_len) receive the result."""
-    import torch
-    i32 = torch.int32
-    B, n = tokens.shape
-    V, t = target.shape[-1], target.dtype
-    if t not in (torch.float32, torch.bfloat16):
-        raise ValueError("target must be fp32 or bf16")
-    _want("tokens", tokens, (B, n), i32)
-    _want("target", target, (B, n, V), t)
-    if draft is not None:
-        _want("draft", draft, (B, n, V), t)
-    _want("u", u, (B, n), torch.float32)
-    _want("path", path, (B, n), i32)
-    _want("n_path", n_path, (B,), i32)
-    _want("out_tokens", out_tokens, (B, n), i32)
-    if tree_mask is not None:
-        _want("tree_mask", tree_mask, (B, n), torch.int64, torch.uint64)
-    if n_nodes is not None:
-        _want("n_nodes", n_nodes, (B,), i32)
-    if (kv_len is None) != (kv_len_out is None):
-        raise ValueError("kv_len and kv_len_out must be given together")
-    if kv_len is not None:
-        _want("kv_len", kv_len, (B,), i32)
-        _want("kv_len_out", kv_len_out, (B,), i32)
-    _launch("infllmv2_verify", (tokens, target, draft, u, path, n_path, out_tokens, tree_mask, n_nodes, kv_len,
-                                kv_len_out), stream, tokens.data_ptr(), _addr(tree_mask), _addr(n_nodes),
-            target.data_ptr(), _addr(draft), u.data_ptr(), _addr(kv_len), B, n, V, FP32 if t == torch.float32 else BF16,
-            1 if replace else 0, path.data_ptr(), n_path.data_ptr(), out_tokens.data_ptr(), _addr(kv_len_out))
+    _check(_binding().verify(tokens, target, draft, u, path, n_path, out_tokens, tree_mask, n_nodes, kv_len, kv_len_out,
+                             replace, stream), "infllmv2_verify")
 
 
 def commit(draft_k, draft_v, path, n_path, k_cache, v_cache, kernel_cache, kv_len, params, stream=None):
     """The path's drafts become the last n_path tokens of the caches (kv_len counts them), and the
     semantic kernels they complete are pooled."""
-    import torch
-    bf16 = torch.bfloat16
-    B, Hkv, n, d = draft_k.shape
-    L_max = k_cache.shape[2]
-    M_max = 0 if kernel_cache is None else kernel_cache.shape[2]
-    _want("draft_k", draft_k, (B, Hkv, n, d), bf16)
-    _want("draft_v", draft_v, (B, Hkv, n, d), bf16)
-    _want("path", path, (B, n), torch.int32)
-    _want("n_path", n_path, (B,), torch.int32)
-    _want("k_cache", k_cache, (B, Hkv, L_max, d), bf16)
-    _want("v_cache", v_cache, (B, Hkv, L_max, d), bf16)
-    if kernel_cache is not None:
-        _want("kernel_cache", kernel_cache, (B, Hkv, M_max, d), bf16)
-    _want("kv_len", kv_len, (B,), torch.int32)
-    _launch("infllmv2_commit", (draft_k, draft_v, path, n_path, k_cache, v_cache, kernel_cache, kv_len), stream,
-            draft_k.data_ptr(), draft_v.data_ptr(), path.data_ptr(), n_path.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), _addr(kernel_cache), kv_len.data_ptr(), B, n, Hkv, d, L_max, M_max,
-            ctypes.byref(Params.make(params)))
+    _check(_binding().commit(draft_k, draft_v, path, n_path, k_cache, v_cache, kernel_cache, kv_len, params, stream),
+           "infllmv2_commit")

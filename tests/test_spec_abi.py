@@ -246,10 +246,34 @@ def test_binding_refuses_types_shapes_and_cpu_tensors(built_lib, name):
 
 def test_binding_takes_fused_slices_and_refuses_uneven_rows(built_lib):
     import torch
-    x = torch.zeros(2, 4, 8, 64, dtype=torch.bfloat16)
-    assert L._head_rows("q", x[..., :4, :], (2, 4), torch.bfloat16, 64) == (4, 512)
-    assert L._head_rows("q", x[:, :1, 4:], (2, 1), torch.bfloat16, 64) == (4, 2048)
-    assert L._head_rows("q", x[:1, :1, 4:], (1, 1), torch.bfloat16, 64) == (4, 256)
-    for bad in (x[:, :3], x[..., ::2, :], x[..., :32], x.transpose(1, 2)):
-        with pytest.raises(ValueError):
-            L._head_rows("q", bad, bad.shape[:-2], torch.bfloat16, bad.shape[-1] if bad.shape[-1] == 32 else 64)
+    bf = torch.bfloat16
+
+    def call(q, B, T):
+        a = _tensors()["rope_append"]
+        new = lambda h: torch.zeros(B, T, h, 64, dtype=bf)  # noqa: E731
+        a.update(q=q, k_new=new(2), v_new=new(2), q_out=torch.zeros(q.shape, dtype=bf), k_cache=torch.zeros(B, 2, 32, 64, dtype=bf),
+                 v_cache=torch.zeros(B, 2, 32, 64, dtype=bf), kv_len=torch.zeros(B, dtype=torch.int32))
+        L.rope_append(**a)
+
+    x = torch.zeros(2, 4, 8, 64, dtype=bf)
+    for q in (x[..., :4, :], x[:, :1, 4:], x[:1, :1, 4:], x[:, :, :1], x[:1]):  # all checks but the device's pass
+        with pytest.raises(ValueError, match="CUDA device"):
+            call(q, *q.shape[:2])
+    for q in (x[:, :3], x[..., ::2, :], x.transpose(0, 1), x.expand(2, 4, 8, 64)[:, :, :1].expand(2, 4, 8, 64)):
+        with pytest.raises(ValueError, match="evenly spaced|dense heads"):
+            call(q, *q.shape[:2])
+
+
+def test_binding_takes_parameters_as_dicts_and_structures(built_lib):
+    a = _tensors()
+    for rope in (dict(rotary_dim=64), L.RopeParams.make(dict(rotary_dim=64, interleaved=1, attn_scale=1.5))):
+        with pytest.raises(ValueError, match="CUDA device"):
+            L.rope(**dict(a["rope"], rope=rope))
+    with pytest.raises(ValueError, match="CUDA device"):
+        L.commit(**dict(a["commit"], params=L.Params.make(P)))
+    with pytest.raises(KeyError):
+        L.rope(**dict(a["rope"], rope=dict(interleaved=1)))
+    with pytest.raises(ValueError, match="parameter structure"):
+        L.rope(**dict(a["rope"], rope=L.Params.make(P)))
+    with pytest.raises(ValueError, match="freqs"):
+        L.rope(**dict(a["rope"], rope=dict(rotary_dim=32)))
