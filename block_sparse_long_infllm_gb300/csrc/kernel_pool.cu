@@ -148,6 +148,8 @@ __global__ void __launch_bounds__(2 * D) commit_kernel(
     constexpr int kChunks = D / 8;
     __shared__ int path_s[64];
     const int bg = blockIdx.x, b = bg / Hkv, tid = threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
     const int m = n_path[b], L = kv_len[b];
     const int j_last = L >= c ? (L - c) / s : -1;
     const int num = L - m - c + 1;  // kernels ending at or after the first committed token
@@ -192,13 +194,8 @@ cudaError_t launch_commit(const void* draft_k, const void* draft_v, const int* p
     auto* kc = static_cast<__nv_bfloat16*>(k_cache);
     auto* vc = static_cast<__nv_bfloat16*>(v_cache);
     auto* kp = static_cast<__nv_bfloat16*>(kernel_cache);
-    if (d == 128)
-        commit_kernel<128><<<grid, 256, 0, stream>>>(dk, dv, path, n_path, kc, vc, kp, kv_len, n_draft, Hkv, L_max, M_max,
-                                                     c, s, err);
-    else
-        commit_kernel<64><<<grid, 128, 0, stream>>>(dk, dv, path, n_path, kc, vc, kp, kv_len, n_draft, Hkv, L_max, M_max,
-                                                    c, s, err);
-    return cudaGetLastError();
+    return launch_kernel(d == 128 ? commit_kernel<128> : commit_kernel<64>, grid, dim3(2 * d), 0, stream, true, dk, dv, path,
+                         n_path, kc, vc, kp, kv_len, n_draft, Hkv, L_max, M_max, c, s, err);
 }
 
 cudaError_t launch_kernel_pool(const void* k_cache, void* kernel_cache, int B, int Hkv, int L_max,

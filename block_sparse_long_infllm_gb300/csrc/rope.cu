@@ -9,7 +9,10 @@
 // 2^64, is the exact fraction of a turn for any 32-bit position, so a far position loses nothing
 // (in fp32 the angle of position 10^6 would be off by up to 0.03 radians).
 //
-// What bounds it is memory: every element is read once and written once.
+// What bounds it is memory: every element is read once and written once.  4 prompts of 16384 tokens of
+// 32 + 2 + 2 heads of 128, bf16: 176 us, 6.85 TB/s; a decode step of 4 rows: 2.0 us, a launch's latency.
+// The launches carry programmatic stream serialisation, so a call's start-up overlaps the tail of the one
+// before (0.3 to 0.5 us of a small call).
 #include "internal.h"
 
 namespace infllmv2 {
@@ -17,36 +20,58 @@ namespace infllmv2 {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kSms = 152;
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T x);
-template <>
-__device__ __forceinline__ float to_f32<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T>
-__device__ __forceinline__ T from_f32(float x);
-template <>
-__device__ __forceinline__ float from_f32<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// VEC consecutive elements, moved as one access.
+// W consecutive 4-byte words, moved as one access.
+template <int W>
+struct alignas(W * 4) Words {
+    uint32_t w[W];
+};
+// VEC consecutive elements of a type, as they lie in memory and as fp32.  Vectors of 16 bytes (8 bytes for
+// the bf16 results of fp32 inputs), or single elements.
 template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Vec {
-    T v[VEC];
+struct Vec {
+    Words<VEC * static_cast<int>(sizeof(T)) / 4> m;
+    __device__ __forceinline__ void load(const T* p) { m = *reinterpret_cast<const decltype(m)*>(p); }
+    __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<decltype(m)*>(p) = m; }
+    __device__ __forceinline__ float get(int e) const {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(m.w[e]);
+        else
+            return (e & 1) ? bf16_hi(m.w[e >> 1]) : bf16_lo(m.w[e >> 1]);
+    }
+    __device__ __forceinline__ void set(const float (&x)[VEC]) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) m.w[e] = __float_as_uint(x[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; e += 2) m.w[e >> 1] = pack_bf16x2(x[e], x[e + 1]);
+        }
+    }
+};
+template <>
+struct Vec<__nv_bfloat16, 1> {
+    uint16_t m;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { m = *reinterpret_cast<const uint16_t*>(p); }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint16_t*>(p) = m; }
+    __device__ __forceinline__ float get(int) const { return bf16_lo(m); }
+    __device__ __forceinline__ void set(const float (&x)[1]) { m = __bfloat16_as_ushort(__float2bfloat16_rn(x[0])); }
 };
 
 template <typename Tin, typename Tout, int VEC>
 __device__ __forceinline__ Vec<Tout, VEC> convert(const Vec<Tin, VEC>& x) {
+    Vec<Tout, VEC> y;
     if constexpr (sizeof(Tin) == sizeof(Tout)) {
-        return x;  // a copy keeps every bit
+        y.m = x.m;  // a copy keeps every bit
     } else {
-        Vec<Tout, VEC> y;
+        float f[VEC];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) y.v[e] = from_f32<Tout>(to_f32(x.v[e]));
-        return y;
+        for (int e = 0; e < VEC; ++e) f[e] = x.get(e);
+        y.set(f);
     }
+    return y;
 }
 
 struct Row {
@@ -114,36 +139,41 @@ __device__ __forceinline__ void check_offsets(const RopeArgs& a) {
     if (bad) raise_error(a.err, kDevErrIndex);
 }
 
+// How a type's rows are spread: heads that a thread loads together, rows that a CTA takes at most, CTAs
+// per SM that the registers have to allow.  Measured on 4 x 16384 tokens of 32 + 2 + 2 heads of 128
+// (1.21 GB, 180 us at the copy rate) for bf16, us: heads 3, rows 8, 3 CTAs 175; 1, 4, 5: 190; 2, 8, 4:
+// 184; 3, 8, 4 (spills): 198; 5, 8, 2: 190.  On the gradient of a 4096-token chunk (113 MB, 16.9 us) for
+// fp32: heads 3, rows 4, 4 CTAs 20.3; 1, 4, 5: 23.6; 4, 4, 4: 24.8; 3, 4, 5 (spills): 29.5.
+template <typename T>
+struct Plan;
+template <>
+struct Plan<__nv_bfloat16> {
+    static constexpr int kHeads = 3, kRows = 8, kResident = 3;
+};
+template <>
+struct Plan<float> {
+    static constexpr int kHeads = 3, kRows = 4, kResident = 4;
+};
+
 // One CTA takes T rows.  A thread keeps one row and one place j of the heads (two vectors of VEC
-// elements) and walks over the heads, so its sines and cosines are loaded once.
-template <int FORM, typename Tin, typename Tout, int VEC>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a, int T) {
+// elements) and walks over the heads, so its sines and cosines are loaded once.  kEarly: the first
+// heads' loads are under way while the row is located and its angles are computed.
+template <int FORM, typename Tin, typename Tout, int VEC, bool kEarly>
+__global__ void __launch_bounds__(kRopeThreads, Plan<Tin>::kResident) rope_kernel(RopeArgs a, int T) {
+    constexpr int kHeads = Plan<Tin>::kHeads;
+    constexpr bool kFromCache = FORM == kRopeChunkBack, kToCache = FORM == kRopeChunk || FORM == kRopeDrafts;
+    using VI = Vec<Tin, VEC>;
+    using VO = Vec<Tout, VEC>;
     extern __shared__ float2 table[];  // [T][rot / 2] (cos, sin)
     __shared__ Row rows_s[kRopeThreads];
     const int tid = threadIdx.x;
     const int r0 = blockIdx.x * T;
     const int half = a.rot / 2;
-    if (tid < T) rows_s[tid] = locate<FORM>(a, r0 + tid);
-    if constexpr (FORM == kRopeChunk || FORM == kRopeChunkBack)
-        if (blockIdx.x == 0 && a.cu_q != nullptr) check_offsets(a);
-    __syncthreads();
-    for (int i = tid; i < T * half; i += kRopeThreads) {
-        const int t = i / half, pair = i % half;
-        const unsigned long long turn =
-            a.freqs[pair] * static_cast<unsigned long long>(static_cast<long long>(rows_s[t].pos));
-        float sn, cs;
-        // the top 32 bits as a signed fraction of half a turn
-        sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &sn, &cs);
-        table[i] = make_float2(cs * a.scale, (a.transposed ? -sn : sn) * a.scale);
-    }
-    __syncthreads();
     const int J = a.d / (2 * VEC);             // places of a head
     const int per_row = kRopeThreads / J / T;  // heads of a row in flight
     const int j = tid % J, slot = tid / J;
-    const int t = slot / per_row;
-    if (t >= T) return;
-    const Row row = rows_s[t];
-    if (!row.ok) return;
+    const int t = slot / per_row;  // < T: T divides the slots
+    const long long r = r0 + t, per_head = static_cast<long long>(a.L_max) * a.d;
     const int rt = a.rot / (2 * VEC);
     const bool turns = j < rt;
     int ea, eb;
@@ -157,6 +187,44 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a, int T) {
         ea = j * VEC;
         eb = half + ea;
     }
+    const int Hqk = a.Hq + a.Hk, heads = Hqk + a.Hv, first = slot % per_row;
+    const Tin* const q = static_cast<const Tin*>(a.q) + r * a.ld_q;
+    const Tin* k = static_cast<const Tin*>(a.k) + (kFromCache ? 0 : r * a.ld_k);
+    const Tin* v = static_cast<const Tin*>(a.v) + (kFromCache ? 0 : r * a.ld_v);
+    VI A[kHeads], B[kHeads];
+    // heads h0, h0 + per_row, ... below `end`, from `begin` on
+    const auto load = [&](int h0, int begin, int end) {
+#pragma unroll
+        for (int u = 0; u < kHeads; ++u) {
+            const int h = h0 + u * per_row;
+            if (h < begin || h >= end) continue;
+            const bool is_q = h < a.Hq, is_k = h < Hqk;
+            const Tin* src = is_q ? q : is_k ? k : v;
+            src += (is_q ? h : is_k ? h - a.Hq : h - Hqk) * (kFromCache && !is_q ? per_head : a.d);
+            A[u].load(src + ea);
+            B[u].load(src + eb);
+        }
+    };
+    pdl_wait();
+    pdl_trigger();
+    // (a row past the last one has nothing to load; one that turns out bad is only read)
+    if (kEarly && r < a.rows) load(first, 0, kFromCache ? a.Hq : heads);
+    if (tid < T) rows_s[tid] = locate<FORM>(a, r0 + tid);
+    if constexpr (FORM == kRopeChunk || FORM == kRopeChunkBack)
+        if (blockIdx.x == 0 && a.cu_q != nullptr) check_offsets(a);
+    __syncthreads();
+    for (int i = tid; i < T * half; i += kRopeThreads) {
+        const int rr = i / half, pair = i % half;
+        const unsigned long long turn =
+            a.freqs[pair] * static_cast<unsigned long long>(static_cast<long long>(rows_s[rr].pos));
+        float sn, cs;
+        // the top 32 bits as a signed fraction of half a turn
+        sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &sn, &cs);
+        table[i] = make_float2(cs * a.scale, (a.transposed ? -sn : sn) * a.scale);
+    }
+    __syncthreads();
+    const Row row = rows_s[t];
+    if (!row.ok) return;
     float cs[VEC], sn[VEC];
     if (turns) {
 #pragma unroll
@@ -166,69 +234,69 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a, int T) {
             sn[e] = w.y;
         }
     }
-    using VI = Vec<Tin, VEC>;
-    using VO = Vec<Tout, VEC>;
-    const long long r = r0 + t;
-    const int heads = a.Hq + a.Hk + a.Hv;
-    for (int h = slot % per_row; h < heads; h += per_row) {
-        const Tin* src;
-        Tout* dst;
-        if (h < a.Hq) {
-            src = static_cast<const Tin*>(a.q) + r * a.ld_q + h * a.d;
-            dst = static_cast<Tout*>(a.q_out) + r * a.ld_qo + h * a.d;
-        } else {
-            const bool is_k = h < a.Hq + a.Hk;
-            const int g = is_k ? h - a.Hq : h - a.Hq - a.Hk;
-            const Tin* s = static_cast<const Tin*>(is_k ? a.k : a.v);
-            Tout* o = static_cast<Tout*>(is_k ? a.k_out : a.v_out);
-            if constexpr (FORM == kRopeChunkBack) {
-                src = s + row.cache + static_cast<long long>(g) * a.L_max * a.d;
-            } else {
-                src = s + r * (is_k ? a.ld_k : a.ld_v) + g * a.d;
-            }
-            if constexpr (FORM == kRopeChunk || FORM == kRopeDrafts) {
-                dst = o + row.cache + static_cast<long long>(g) * a.L_max * a.d;
-            } else {
-                dst = o + r * (is_k ? a.ld_ko : a.ld_vo) + g * a.d;
-            }
-        }
-        const VI A = *reinterpret_cast<const VI*>(src + ea), B = *reinterpret_cast<const VI*>(src + eb);
-        VO X, Y;
-        if (!turns || h >= a.Hq + a.Hk) {
-            X = convert<Tin, Tout, VEC>(A);
-            Y = convert<Tin, Tout, VEC>(B);
-        } else if (a.interleaved) {
+    if constexpr (kFromCache) {
+        k += row.cache;
+        v += row.cache;
+    }
+    Tout* const qo = static_cast<Tout*>(a.q_out) + r * a.ld_qo;
+    Tout* const ko = static_cast<Tout*>(a.k_out) + (kToCache ? row.cache : r * a.ld_ko);
+    Tout* const vo = static_cast<Tout*>(a.v_out) + (kToCache ? row.cache : r * a.ld_vo);
+    for (int h0 = first; h0 < heads; h0 += kHeads * per_row) {
+        if (!kEarly || h0 != first) load(h0, 0, heads);
+        if (kEarly && kFromCache && h0 == first) load(h0, a.Hq, heads);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {  // pair e is elements 2e, 2e + 1 of A followed by B
-                const int i0 = 2 * e, i1 = 2 * e + 1;
-                const float x = to_f32(i0 < VEC ? A.v[i0 % VEC] : B.v[i0 % VEC]);
-                const float y = to_f32(i1 < VEC ? A.v[i1 % VEC] : B.v[i1 % VEC]);
-                const Tout fx = from_f32<Tout>(x * cs[e] - y * sn[e]), fy = from_f32<Tout>(x * sn[e] + y * cs[e]);
-                if (i0 < VEC) X.v[i0 % VEC] = fx; else Y.v[i0 % VEC] = fx;
-                if (i1 < VEC) X.v[i1 % VEC] = fy; else Y.v[i1 % VEC] = fy;
-            }
-        } else {
+        for (int u = 0; u < kHeads; ++u) {
+            const int h = h0 + u * per_row;
+            if (h >= heads) continue;
+            const bool is_q = h < a.Hq, is_k = h < Hqk;
+            Tout* dst = is_q ? qo : is_k ? ko : vo;
+            dst += (is_q ? h : is_k ? h - a.Hq : h - Hqk) * (kToCache && !is_q ? per_head : a.d);
+            VO X, Y;
+            if (!turns || !is_k) {
+                X = convert<Tin, Tout, VEC>(A[u]);
+                Y = convert<Tin, Tout, VEC>(B[u]);
+            } else {
+                float x[VEC], y[VEC];
+                if (a.interleaved) {  // pair e is elements 2e, 2e + 1 of A followed by B
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float x = to_f32(A.v[e]), y = to_f32(B.v[e]);
-                X.v[e] = from_f32<Tout>(x * cs[e] - y * sn[e]);
-                Y.v[e] = from_f32<Tout>(x * sn[e] + y * cs[e]);
+                    for (int e = 0; e < VEC; ++e) {
+                        const int i = 2 * e, j2 = 2 * e + 1;
+                        const float m = i < VEC ? A[u].get(i % VEC) : B[u].get(i % VEC);
+                        const float n = j2 < VEC ? A[u].get(j2 % VEC) : B[u].get(j2 % VEC);
+                        const float fm = m * cs[e] - n * sn[e], fn = m * sn[e] + n * cs[e];
+                        if (i < VEC) x[i % VEC] = fm; else y[i % VEC] = fm;
+                        if (j2 < VEC) x[j2 % VEC] = fn; else y[j2 % VEC] = fn;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float m = A[u].get(e), n = B[u].get(e);
+                        x[e] = m * cs[e] - n * sn[e];
+                        y[e] = m * sn[e] + n * cs[e];
+                    }
+                }
+                X.set(x);
+                Y.set(y);
             }
+            X.store(dst + ea);
+            Y.store(dst + eb);
         }
-        *reinterpret_cast<VO*>(dst + ea) = X;
-        *reinterpret_cast<VO*>(dst + eb) = Y;
     }
 }
 
 template <int FORM, typename Tin, typename Tout, int VEC>
 cudaError_t launch(const RopeArgs& a) {
+    // rows a CTA takes: fewer where that leaves SMs without work
     const int slots = kRopeThreads / (a.d / (2 * VEC));
-    int T = slots < 4 ? slots : 4;  // rows a CTA takes
-    if (a.rows < 4 * 152) T = 1;
-    const int grid = (a.rows + T - 1) / T;
-    rope_kernel<FORM, Tin, Tout, VEC>
-        <<<grid, kRopeThreads, static_cast<size_t>(T) * (a.rot / 2) * sizeof(float2), a.stream>>>(a, T);
-    return cudaGetLastError();
+    int T = slots < Plan<Tin>::kRows ? slots : Plan<Tin>::kRows;
+    while (T > 1 && a.rows < T * 2 * kSms) T /= 2;
+    const int grid = (a.rows - 1) / T + 1;
+    const size_t smem = static_cast<size_t>(T) * (a.rot / 2) * sizeof(float2);
+    // Loading before the row is located shortens a call of few CTAs (4 rows 2.34 -> 2.03 us, 16 drafts 2.8
+    // -> 2.5) but costs the larger ones, where other CTAs fill the wait (16384-token prompts 175 -> 198 us).
+    const bool early = grid <= 2 * kSms;
+    return launch_kernel(early ? rope_kernel<FORM, Tin, Tout, VEC, true> : rope_kernel<FORM, Tin, Tout, VEC, false>,
+                         dim3(grid), dim3(kRopeThreads), smem, a.stream, true, a, T);
 }
 
 // Vectors of 16 bytes where both halves of the rotated part and every row start on a vector's

@@ -393,6 +393,8 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
         sh.stands = 0ull;
     }
     if (tid < 64) sh.kids[tid] = 0ull;
+    pdl_wait();
+    pdl_trigger();
     const int n = a.n_nodes != nullptr ? a.n_nodes[b] : a.n;
     bool bad = n < 0 || n > a.n;
     if (tid < a.n) {
@@ -616,12 +618,14 @@ cudaError_t launch(const VerifyArgs& a) {
     cfg.gridDim = dim3(static_cast<unsigned>(a.B) * CL);
     cfg.blockDim = dim3(kVerifyThreads);
     cfg.stream = a.stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = CL;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, verify_kernel<T>, a, CL);
 }
 
