@@ -137,11 +137,15 @@ cudaError_t launch_append(const void* k_new, const void* v_new, void* k_cache, v
 // Commit of accepted drafts ("MiniCPM4: 如何在手机电脑上高效运行大语言模型", section 1.1, tree-speculative
 // decoding; static caches of "CPM.cu：端侧大模型推理的 CUDA 加速引擎", section 4): the K and V of the
 // path's drafts into the last n_path rows of each sequence's caches, and the semantic kernels that
-// these tokens complete, as kernel_pool_kernel computes them.  CTAs of blockIdx.y 0 copy; each other
-// one pools one kernel, taking the rows being committed from the draft buffer, so that no CTA reads
-// what another writes.
-template <int D>
-__global__ void __launch_bounds__(2 * D) commit_kernel(
+// these tokens complete, as kernel_pool_kernel computes them.  CTAs of blockIdx.y 0 copy; each other one pools
+// one kernel, taking the rows being committed from the draft buffer, so that no CTA reads
+// what another writes.  What bounds it is latency: two dependent
+// loads (the path, then rows) and the pooling's chain of shuffles, 2.3 us for one sequence of 16 drafts;
+// for many sequences also how many CTAs are resident, so kernels of at most 32 tokens (the pages' size)
+// have their own instance with two rows per lane (48 registers instead of 120): 32 sequences x 8 heads
+// of 64 drafts 8.5 us.  Pooling two (four) kernels per CTA, with fewer CTAs, took 11.1 (14.2) us.
+template <int D, int kRows>
+__global__ void __launch_bounds__(2 * D, kRows == 2 ? 640 / D : 1) commit_kernel(
     const __nv_bfloat16* __restrict__ dk, const __nv_bfloat16* __restrict__ dv, const int* __restrict__ path,
     const int* __restrict__ n_path, __nv_bfloat16* k, __nv_bfloat16* __restrict__ v, __nv_bfloat16* __restrict__ kern,
     const int* __restrict__ kv_len, int n, int Hkv, int L_max, int M_max, int c, int s, int* __restrict__ err) {
@@ -151,33 +155,46 @@ __global__ void __launch_bounds__(2 * D) commit_kernel(
     pdl_wait();
     pdl_trigger();
     const int m = n_path[b], L = kv_len[b];
+    const int i_path = tid < n ? path[static_cast<size_t>(b) * n + tid] : 0;
     const int j_last = L >= c ? (L - c) / s : -1;
     const int num = L - m - c + 1;  // kernels ending at or after the first committed token
     const int j_first = num <= 0 ? 0 : (num + s - 1) / s;
+    const int j = j_first + static_cast<int>(blockIdx.y) - 1;
     bool bad = m < 0 || m > n || L < m || L > L_max || (m > 0 && j_last >= j_first && j_last >= M_max);
-    if (!bad && tid < m) {
-        const int i = path[static_cast<size_t>(b) * n + tid];
-        path_s[tid] = i;
-        bad = i < 0 || i >= n;
-    }
+    if (blockIdx.y != 0 && (bad || m == 0 || j > j_last)) return;  // no such kernel (the copying CTAs report)
+    bad = bad || (tid < m && (i_path < 0 || i_path >= n));
+    if (tid < m && tid < 64) path_s[tid] = i_path;
     if (__syncthreads_or(bad)) {
         if (tid == 0 && blockIdx.y == 0) raise_error(err, kDevErrIndex);
         return;
     }
     const size_t src0 = static_cast<size_t>(bg) * n, row0 = static_cast<size_t>(bg) * L_max;
     if (blockIdx.y == 0) {
-        for (int i = tid; i < m * kChunks; i += 2 * D) {
-            const int t = i / kChunks, ch = i % kChunks;
-            const size_t from = (src0 + path_s[t]) * kChunks + ch, to = (row0 + (L - m) + t) * kChunks + ch;
-            reinterpret_cast<uint4*>(k)[to] = ldg_v4(reinterpret_cast<const uint4*>(dk) + from);
-            reinterpret_cast<uint4*>(v)[to] = ldg_v4(reinterpret_cast<const uint4*>(dv) + from);
+        const uint4 *const ks = reinterpret_cast<const uint4*>(dk) + src0 * kChunks,
+                    *const vs = reinterpret_cast<const uint4*>(dv) + src0 * kChunks;
+        uint4 *const kd = reinterpret_cast<uint4*>(k) + (row0 + (L - m)) * kChunks,
+              *const vd = reinterpret_cast<uint4*>(v) + (row0 + (L - m)) * kChunks;
+        constexpr int kCopies = 64 * kChunks / (2 * D);  // of a thread, for a path of 64: all in flight
+        uint4 x[kCopies], y[kCopies];
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const int at = tid + i * 2 * D;
+            if (at >= m * kChunks) continue;
+            const int from = path_s[at / kChunks] * kChunks + at % kChunks;
+            x[i] = ldg_v4(ks + from);
+            y[i] = ldg_v4(vs + from);
+        }
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const int at = tid + i * 2 * D;
+            if (at >= m * kChunks) continue;
+            kd[at] = x[i];
+            vd[at] = y[i];
         }
         return;
     }
-    const int j = j_first + static_cast<int>(blockIdx.y) - 1;
-    if (m == 0 || j > j_last) return;
     const int ch = tid / kMeanLanes, ln = tid % kMeanLanes;
-    const uint4 r = exact_mean_rows(c, ln, [&](int i) {
+    const uint4 r = exact_mean_rows<kRows>(c, ln, [&](int i) {
         const int x = j * s + i, t = x - (L - m);  // t at or past 0: a committed row
         return t >= 0 ? ldg_v4(reinterpret_cast<const uint4*>(dk) + (src0 + path_s[t]) * kChunks + ch)
                       : ldg_v4(reinterpret_cast<const uint4*>(k) + (row0 + x) * kChunks + ch);
@@ -194,8 +211,11 @@ cudaError_t launch_commit(const void* draft_k, const void* draft_v, const int* p
     auto* kc = static_cast<__nv_bfloat16*>(k_cache);
     auto* vc = static_cast<__nv_bfloat16*>(v_cache);
     auto* kp = static_cast<__nv_bfloat16*>(kernel_cache);
-    return launch_kernel(d == 128 ? commit_kernel<128> : commit_kernel<64>, grid, dim3(2 * d), 0, stream, true, dk, dv, path,
-                         n_path, kc, vc, kp, kv_len, n_draft, Hkv, L_max, M_max, c, s, err);
+    const bool small = c <= 2 * kMeanLanes;
+    const auto kernel = d == 128 ? (small ? commit_kernel<128, 2> : commit_kernel<128, kMeanRows>)
+                                 : (small ? commit_kernel<64, 2> : commit_kernel<64, kMeanRows>);
+    return launch_kernel(kernel, grid, dim3(2 * d), 0, stream, true, dk, dv, path, n_path, kc, vc, kp, kv_len, n_draft, Hkv,
+                         L_max, M_max, c, s, err);
 }
 
 cudaError_t launch_kernel_pool(const void* k_cache, void* kernel_cache, int B, int Hkv, int L_max,

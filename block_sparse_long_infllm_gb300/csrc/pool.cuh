@@ -47,15 +47,21 @@ __device__ __forceinline__ uint32_t bf16_of_ratio(unsigned long long A, int c, i
     return sign | (static_cast<uint32_t>(ef) << 7) | static_cast<uint32_t>(top & 127ull);
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Exact mean of the c rows of one 8-element slice; lane ln (of the 16 aligned lanes sharing the
-// slice) takes rows ln, ln + 16, ... from row(i).  Every lane of the group returns the 8 bf16
-// results, packed.
-template <typename RowOf>
+// slice) takes rows ln, ln + 16, ... (at most kRows of them) from row(i).  Every lane of the group
+// returns the 8 bf16 results, packed.
+template <int kRows = kMeanRows, typename RowOf>
 __device__ __forceinline__ uint4 exact_mean_rows(int c, int ln, RowOf row) {
-    uint32_t w[kMeanRows][4];
+    uint32_t w[kRows][4];
     const int n_u = (c + kMeanLanes - 1) / kMeanLanes;  // row rounds any lane of the group has
 #pragma unroll
-    for (int u = 0; u < kMeanRows; ++u) {
+    for (int u = 0; u < kRows; ++u) {
         const int i = ln + kMeanLanes * u;
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
         if (u < n_u && i < c) x = row(i);
@@ -64,49 +70,59 @@ __device__ __forceinline__ uint4 exact_mean_rows(int c, int ln, RowOf row) {
         w[u][2] = x.z;
         w[u][3] = x.w;
     }
-    int emax[8];  // largest biased exponent per column (1 for zeros and subnormals)
+    // largest biased exponent per column (1 for zeros and subnormals), two columns to a word in place
+    uint32_t xm2[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) emax[e] = 1;
+    for (int i = 0; i < 4; ++i) xm2[i] = 0x00800080u;
 #pragma unroll
-    for (int u = 0; u < kMeanRows; ++u) {
+    for (int u = 0; u < kRows; ++u) {
         if (u >= n_u) break;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) emax[e] = max(emax[e], static_cast<int>((w[u][e >> 1] >> (16 * (e & 1) + 7)) & 0xFFu));
+        for (int i = 0; i < 4; ++i) xm2[i] = max_u16x2(xm2[i], w[u][i] & 0x7F807F80u);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int off = 1; off < kMeanLanes; off <<= 1)
 #pragma unroll
-        for (int off = 1; off < kMeanLanes; off <<= 1) emax[e] = max(emax[e], __shfl_xor_sync(0xffffffffu, emax[e], off));
+        for (int i = 0; i < 4; ++i) xm2[i] = max_u16x2(xm2[i], __shfl_xor_sync(0xffffffffu, xm2[i], off));
+    int emax[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) emax[e] = static_cast<int>((xm2[e >> 1] >> (16 * (e & 1) + 7)) & 0xFFu);
     long long S[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) S[e] = 0;
 #pragma unroll
-    for (int u = 0; u < kMeanRows; ++u) {
+    for (int u = 0; u < kRows; ++u) {
         if (u >= n_u) break;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const uint32_t h = (w[u][e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
             const int ef = static_cast<int>((h >> 7) & 0xFFu);
-            const long long mant = ef != 0 ? static_cast<long long>(128u | (h & 127u)) : static_cast<long long>(h & 127u);
-            const int sh = max(ef, 1) - (emax[e] - 40);  // value = mant * 2^(max(ef,1) - 134)
-            const long long v = sh >= 0 ? (mant << sh) : (mant >> min(-sh, 62));
-            S[e] += (h & 0x8000u) ? -v : v;
+            const uint32_t mant = (h & 127u) | (ef != 0 ? 128u : 0u);
+            const int sh = max(ef, 1) - (emax[e] - 40);  // value = mant * 2^(max(ef,1) - 134); sh <= 40
+            // +-(mant << sh), bits below 1 dropped, added by one multiply-add: the mantissa is shifted right
+            // (from 10 places up) or multiplied by a power of two up to 2^30
+            const int mag = static_cast<int>((mant << 10) >> min(max(10 - sh, 0), 31));
+            S[e] += static_cast<long long>((h & 0x8000u) ? -mag : mag) * (1 << max(sh - 10, 0));
         }
     }
+    // Sums over the lanes, halving the columns as they go: a lane keeps those that agree with its number in
+    // one bit after another and hands the rest to its neighbour, so lane ln ends with column ln % 8 (16
+    // shuffles of a word instead of 64), which it rounds; the 8 results are then gathered.
+    long long S4[4], S2[2], Sm;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int i = 0; i < 4; ++i) {
+        const long long keep = (ln & 1) ? S[2 * i + 1] : S[2 * i], give = (ln & 1) ? S[2 * i] : S[2 * i + 1];
+        S4[i] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+    }
 #pragma unroll
-        for (int off = 1; off < kMeanLanes; off <<= 1) S[e] += __shfl_xor_sync(0xffffffffu, S[e], off);
-    // lane ln rounds column ln % 8 of the group's sums; the 8 results are then gathered
-    const int em = ln & 7;
-    long long Sm = S[0];
-    int xm = emax[0];
-#pragma unroll
-    for (int e = 1; e < 8; ++e)
-        if (e == em) {
-            Sm = S[e];
-            xm = emax[e];
-        }
+    for (int i = 0; i < 2; ++i) {
+        const long long keep = (ln & 2) ? S4[2 * i + 1] : S4[2 * i], give = (ln & 2) ? S4[2 * i] : S4[2 * i + 1];
+        S2[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+    }
+    Sm = ((ln & 4) ? S2[1] : S2[0]) + __shfl_xor_sync(0xffffffffu, (ln & 4) ? S2[0] : S2[1], 4);
+    Sm += __shfl_xor_sync(0xffffffffu, Sm, 8);
+    const uint32_t xw = (ln & 4) ? ((ln & 2) ? xm2[3] : xm2[2]) : ((ln & 2) ? xm2[1] : xm2[0]);
+    const int xm = static_cast<int>((xw >> (16 * (ln & 1) + 7)) & 0xFFu);
     const uint32_t bits =
         bf16_of_ratio(static_cast<unsigned long long>(Sm < 0 ? -Sm : Sm), c, xm - 40 - 134, Sm < 0);
     const int g0 = (threadIdx.x & 31) & ~(kMeanLanes - 1);  // first lane of this group in the warp
