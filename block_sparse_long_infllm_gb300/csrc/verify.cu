@@ -33,10 +33,11 @@ namespace {
 
 using u64 = unsigned long long;
 
+#define VB16 16
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kResident = 4;  // CTAs per SM
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kMaxPieces = kMaxCluster * kVerifyWarps;  // pieces of a row: one per warp of the cluster
 constexpr int kLanePieces = kMaxPieces / 32;
 constexpr int kBatch = 4;     // chunks of each row that a lane loads together
@@ -359,8 +360,9 @@ __device__ __forceinline__ Sums sweep(const RowView<T>& P, const RowView<T>& Q, 
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
+            if (it + i >= its) break;
             s.template take<T, KIND>(x[i], KIND != 0 ? y[i] : x[i], c);
-            if (it + i < its && (seg == 1 || (it + i + 1) % seg == 0 || it + i + 1 == its))
+            if (seg == 1 || (it + i + 1) % seg == 0 || it + i + 1 == its)
                 cum[(it + i) / seg][threadIdx.x] = s.p - s.q;
         }
     }
@@ -429,30 +431,59 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
     int drawn = -1;
     if (!idle) {
         // the walk (warp 0)
-        u64 on = 1ull, rest = sh.kids[0], gone = 0ull, Z = kOne;
+        u64 on = 1ull, rest = 0ull, gone = 0ull, Z = kOne, easy = 0ull;
         long long R = static_cast<long long>(kOne);
         Coef c{{0ull, 0}, 0};
         int cur = 0;
         bool fresh = true, z_known = true;  // no child of cur was tried yet; Z belongs to c
+        if (warp == 0) {
+            // nodes that are tried first and stand: a way of nothing but these needs no arithmetic
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = 32 * h + lane;
+                bool yes = i > 0 && i < n && ((sh.stands >> i) & 1ull) != 0ull;
+                if (yes) yes = lowest(sh.kids[63 - __clzll(static_cast<long long>(sh.mask[i] ^ (1ull << i)))]) == i;
+                easy |= static_cast<u64>(__ballot_sync(0xffffffffu, yes)) << (32 * h);
+            }
+        }
         for (int round = 0;; ++round) {
             if (warp == 0) {
-                while (rest != 0ull && z_known) {
+                while (z_known) {
+                    if (fresh) {
+                        // the last node below cur that the easy ones lead to; its first child, if it has one, falls
+                        u64 reach = 0ull;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int i = 32 * h + lane;
+                            const bool yes = i < n && (sh.mask[i] & on) == on && (sh.mask[i] & ~on & ~easy) == 0ull;
+                            reach |= static_cast<u64>(__ballot_sync(0xffffffffu, yes)) << (32 * h);
+                        }
+                        cur = 63 - __clzll(static_cast<long long>(reach));
+                        on = sh.mask[cur];
+                        rest = sh.kids[cur];
+                        if (rest == 0ull) break;
+                        const int i = lowest(rest);
+                        rest &= rest - 1;
+                        fresh = false;
+                        if (draft == nullptr) {
+                            const u64 w = add_fixed(0ull, sh.p[i]);
+                            gone = 1ull << i;
+                            Z = Z > w ? Z - w : 0ull;
+                        } else {
+                            c = Coef{{1ull << 63, 0}, 1};
+                            z_known = false;
+                            if (!a.replace) R -= static_cast<long long>(add_fixed(0ull, sh.q[i]));
+                        }
+                        continue;
+                    }
+                    if (rest == 0ull) break;
                     const int i = lowest(rest);
                     const float q = sh.q[i];
-                    u64 w = 0ull;
-                    bool stand;
-                    if (fresh && draft != nullptr) {
-                        stand = ((sh.stands >> i) & 1ull) != 0ull;
-                    } else {
-                        w = weight(sh.p[i], q, c);  // c = 0 without draft probabilities
-                        for (u64 g = gone; g != 0ull; g &= g - 1)
-                            if (sh.tok[lowest(g)] == sh.tok[i]) w = 0ull;
-                        stand = R > 0 && stands(sh.u[i], Z, q, w, static_cast<u64>(R));
-                    }
-                    if (stand) {
-                        cur = i;
+                    u64 w = weight(sh.p[i], q, c);  // c = 0 without draft probabilities
+                    for (u64 g = gone; g != 0ull; g &= g - 1)
+                        if (sh.tok[lowest(g)] == sh.tok[i]) w = 0ull;
+                    if (R > 0 && stands(sh.u[i], Z, q, w, static_cast<u64>(R))) {
                         on |= 1ull << i;
-                        rest = sh.kids[i];
                         gone = 0ull;
                         c.kind = 0;
                         Z = kOne;
@@ -461,7 +492,6 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
                         continue;
                     }
                     rest &= rest - 1;
-                    fresh = false;
                     if (draft == nullptr) {
                         gone |= 1ull << i;
                         Z = Z > w ? Z - w : 0ull;
@@ -469,8 +499,8 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
                         if (R > 0 && Z != 0ull) {
                             Num z = num(Z);
                             if (R != static_cast<long long>(kOne)) z = divide(z, num(static_cast<u64>(R)));
-                            c.v = c.kind == 0 ? z : add(c.v, z);
-                            c.kind = c.v.m == (1ull << 63) && c.v.e == 0 ? 1 : 2;
+                            c.v = add(c.v, z);
+                            c.kind = 2;  // past 1
                             z_known = false;
                         }
                         if (!a.replace) R -= static_cast<long long>(add_fixed(0ull, q));
@@ -611,7 +641,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
 // whose warps each have at least 32 chunks.
 template <typename T>
 cudaError_t launch(const VerifyArgs& a) {
-    int CL = kMaxCluster;
+    int CL = a.B <= VB16 ? kMaxCluster : 8;
     while (CL > 1 && (static_cast<long long>(a.B) * CL > kResident * 152 || a.V < CL * kVerifyThreads * RowView<T>::N))
         CL /= 2;
     cudaLaunchConfig_t cfg = {};
@@ -622,6 +652,10 @@ cudaError_t launch(const VerifyArgs& a) {
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = CL;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    if (CL > 8) {  // past the portable size
+        const cudaError_t e = cudaFuncSetAttribute(verify_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
