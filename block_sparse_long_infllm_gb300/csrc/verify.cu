@@ -33,9 +33,9 @@ namespace {
 
 using u64 = unsigned long long;
 
-#define VB16 16
 constexpr int kVerifyThreads = 256;
-constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kWarpsLog = 3, kVerifyWarps = 1 << kWarpsLog;
+static_assert(kVerifyWarps * 32 == kVerifyThreads, "");
 constexpr int kResident = 4;  // CTAs per SM
 constexpr int kMaxCluster = 16;
 constexpr int kMaxPieces = kMaxCluster * kVerifyWarps;  // pieces of a row: one per warp of the cluster
@@ -346,6 +346,8 @@ __device__ __forceinline__ Sums sweep(const RowView<T>& P, const RowView<T>& Q, 
                                       int seg, u64 (*cum)[kVerifyThreads]) {
     const int lane = threadIdx.x & 31, lo = max(P.lo(), k0), hi = min(P.hi(), k1);
     Sums s;
+    u64* out = &cum[0][threadIdx.x];
+    int left = seg;  // rounds of the segment
     if (k0 == 0 && lo > 0 && lane == 0 && k1 > 0) {  // the row's cut first chunk
         const uint4 x = P.edge(0);
         s.template take<T, KIND>(x, KIND != 0 ? Q.edge(0) : x, c);
@@ -362,8 +364,11 @@ __device__ __forceinline__ Sums sweep(const RowView<T>& P, const RowView<T>& Q, 
         for (int i = 0; i < kBatch; ++i) {
             if (it + i >= its) break;
             s.template take<T, KIND>(x[i], KIND != 0 ? y[i] : x[i], c);
-            if (seg == 1 || (it + i + 1) % seg == 0 || it + i + 1 == its)
-                cum[(it + i) / seg][threadIdx.x] = s.p - s.q;
+            if (--left == 0 || it + i + 1 == its) {
+                *out = s.p - s.q;
+                out += kVerifyThreads;
+                left = seg;
+            }
         }
     }
     const int last = P.chunks() - 1;
@@ -377,10 +382,10 @@ __device__ __forceinline__ Sums sweep(const RowView<T>& P, const RowView<T>& Q, 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(VerifyArgs a, int CL) {
+__global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(VerifyArgs a, int cl_log) {
     constexpr int N = RowView<T>::N;
     __shared__ Shared sh;
-    const int rank = blockIdx.x % CL, b = blockIdx.x / CL;
+    const int CL = 1 << cl_log, rank = blockIdx.x & (CL - 1), b = blockIdx.x >> cl_log;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int pieces = CL * kVerifyWarps, piece = rank * kVerifyWarps + warp;
     const size_t at = static_cast<size_t>(b) * a.n;
@@ -520,7 +525,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
             const int skew = static_cast<int>(((at + node) * a.V) % N);
             const RowView<T> P{target + static_cast<size_t>(node) * a.V, skew, a.V};
             const RowView<T> Q{draft + (draft != nullptr ? static_cast<size_t>(node) * a.V : 0), skew, a.V};
-            const int per_piece = (P.chunks() + pieces - 1) / pieces, its = (per_piece + 31) / 32;
+            const int per_piece = (P.chunks() + pieces - 1) >> (cl_log + kWarpsLog), its = (per_piece + 31) >> 5;
             const int seg = (its + kSegments - 1) / kSegments;
             const int k0 = min(piece * per_piece, P.chunks()), k1 = min(k0 + per_piece, P.chunks());
             const Sums s = cf.kind == 0   ? sweep<T, 0>(P, Q, cf.v, k0, k1, its, seg, sh.cum)
@@ -641,9 +646,11 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
 // whose warps each have at least 32 chunks.
 template <typename T>
 cudaError_t launch(const VerifyArgs& a) {
-    int CL = a.B <= VB16 ? kMaxCluster : 8;
-    while (CL > 1 && (static_cast<long long>(a.B) * CL > kResident * 152 || a.V < CL * kVerifyThreads * RowView<T>::N))
-        CL /= 2;
+    int cl_log = a.B <= 16 ? 4 : 3;
+    while (cl_log > 0 && ((static_cast<long long>(a.B) << cl_log) > kResident * 152 ||
+                          a.V < (kVerifyThreads * RowView<T>::N) << cl_log))
+        --cl_log;
+    const int CL = 1 << cl_log;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.B) * CL);
     cfg.blockDim = dim3(kVerifyThreads);
@@ -660,7 +667,7 @@ cudaError_t launch(const VerifyArgs& a) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, verify_kernel<T>, a, CL);
+    return cudaLaunchKernelEx(&cfg, verify_kernel<T>, a, cl_log);
 }
 
 }  // namespace
