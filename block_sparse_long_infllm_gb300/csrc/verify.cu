@@ -145,19 +145,20 @@ __device__ __forceinline__ bool stands(float u, u64 Z, float q, u64 w, u64 R) {
 // ---- rows
 
 // A row in 16-byte chunks of memory: chunk k holds elements k*N - skew .. of the row, `skew` the row's
-// distance from a 16-byte boundary.
+// distance from a 16-byte boundary.  The first and the last chunk may hold elements of the rows beside
+// it; the last one of the tensor's last row (open_end false) is not read past the tensor.
 template <typename T>
 struct RowView {
     static constexpr int N = 16 / sizeof(T);
     const T* p;
     int skew, V;
-    // Chunks [lo, hi) lie wholly inside the row; one at either end may be cut.
-    __device__ __forceinline__ int lo() const { return skew != 0 ? 1 : 0; }
-    __device__ __forceinline__ int hi() const { return (skew + V) / N; }
+    bool open_end;
     __device__ __forceinline__ int chunks() const { return (skew + V + N - 1) / N; }
+    __device__ __forceinline__ int whole() const { return (skew + V) / N; }  // chunks [skew != 0, whole) are uncut
+    __device__ __forceinline__ int end() const { return open_end ? chunks() : whole(); }  // of those load() reads
     // Chunk k if `want`, else 0.  One predicated load, so that several in a row are in flight together
     // (a branch around each load would make them wait for one another).
-    __device__ __forceinline__ uint4 whole(int k, bool want) const {
+    __device__ __forceinline__ uint4 load(int k, bool want) const {
         uint4 r = make_uint4(0u, 0u, 0u, 0u);
         asm("{\n"
             " .reg .pred p;\n"
@@ -168,17 +169,36 @@ struct RowView {
             : "l"(p - skew + static_cast<long long>(k) * N), "r"(want ? 1 : 0));
         return r;
     }
-    // A cut chunk, element by element; elements outside the row are 0.
-    __device__ __noinline__ uint4 edge(int k) const {
+    __device__ __forceinline__ bool cut(int k) const { return k >= whole() || (k == 0 && skew != 0); }
+    // What a cut chunk holds of other rows becomes 0.
+    __device__ __forceinline__ void trim(uint4& x, int k) const {
+        const int a = k * N - skew;
+        if constexpr (sizeof(T) == 4) {
+            x.x = a >= 0 && a < V ? x.x : 0u;
+            x.y = a + 1 >= 0 && a + 1 < V ? x.y : 0u;
+            x.z = a + 2 >= 0 && a + 2 < V ? x.z : 0u;
+            x.w = a + 3 >= 0 && a + 3 < V ? x.w : 0u;
+        } else {
+            const auto pair = [&](uint32_t w, int i) {
+                return (i >= 0 && i < V ? w & 0xFFFFu : 0u) | (i + 1 >= 0 && i + 1 < V ? w & 0xFFFF0000u : 0u);
+            };
+            x.x = pair(x.x, a);
+            x.y = pair(x.y, a + 2);
+            x.z = pair(x.z, a + 4);
+            x.w = pair(x.w, a + 6);
+        }
+    }
+    // The cut chunk at the end of the tensor, element by element.
+    __device__ __noinline__ uint4 tail() const {
         uint32_t w[4] = {0u, 0u, 0u, 0u};
+        const int a = whole() * N - skew;
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            const int i = k * N - skew + e;
-            if (i < 0 || i >= V) continue;
+            if (a + e < 0 || a + e >= V) continue;
             if constexpr (sizeof(T) == 4)
-                w[e] = __float_as_uint(p[i]);
+                w[e] = __float_as_uint(p[a + e]);
             else
-                w[e >> 1] |= static_cast<uint32_t>(__bfloat16_as_ushort(p[i])) << (16 * (e & 1));
+                w[e >> 1] |= static_cast<uint32_t>(__bfloat16_as_ushort(p[a + e])) << (16 * (e & 1));
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
@@ -295,11 +315,14 @@ struct Weights {
     __device__ __forceinline__ void chunk(int k, int k1, u64 (&w)[N]) const {
 #pragma unroll
         for (int e = 0; e < N; ++e) w[e] = 0ull;
-        const bool in = k >= P.lo() && k < min(k1, P.hi());
-        uint4 x = P.whole(k, in), y = Q.whole(k, in && c.kind != 0);
+        const bool in = k < min(k1, P.end());
+        uint4 x = P.load(k, in), y = Q.load(k, in && c.kind != 0);
         if (k < k1 && !in) {
-            x = P.edge(k);
-            if (c.kind != 0) y = Q.edge(k);
+            x = P.tail();
+            if (c.kind != 0) y = Q.tail();
+        } else if (P.cut(k)) {
+            P.trim(x, k);
+            Q.trim(y, k);
         }
 #pragma unroll
         for (int e = 0; e < N; ++e) w[e] = weight(element<T>(x, e), element<T>(y, e), c);
@@ -344,25 +367,26 @@ struct Weights {
 template <typename T, int KIND>
 __device__ __forceinline__ Sums sweep(const RowView<T>& P, const RowView<T>& Q, const Num& c, int k0, int k1, int its,
                                       int seg, u64 (*cum)[kVerifyThreads]) {
-    const int lane = threadIdx.x & 31, lo = max(P.lo(), k0), hi = min(P.hi(), k1);
+    const int lane = threadIdx.x & 31, hi = min(P.end(), k1);
     Sums s;
     u64* out = &cum[0][threadIdx.x];
     int left = seg;  // rounds of the segment
-    if (k0 == 0 && lo > 0 && lane == 0 && k1 > 0) {  // the row's cut first chunk
-        const uint4 x = P.edge(0);
-        s.template take<T, KIND>(x, KIND != 0 ? Q.edge(0) : x, c);
-    }
     for (int it = 0; it < its; it += kBatch) {
         uint4 x[kBatch], y[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             const int k = k0 + 32 * (it + i) + lane;
-            x[i] = P.whole(k, k >= lo && k < hi);
-            if (KIND != 0) y[i] = Q.whole(k, k >= lo && k < hi);
+            x[i] = P.load(k, k < hi);
+            if (KIND != 0) y[i] = Q.load(k, k < hi);
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             if (it + i >= its) break;
+            const int k = k0 + 32 * (it + i) + lane;
+            if (P.cut(k)) {
+                P.trim(x[i], k);
+                if (KIND != 0) Q.trim(y[i], k);
+            }
             s.template take<T, KIND>(x[i], KIND != 0 ? y[i] : x[i], c);
             if (--left == 0 || it + i + 1 == its) {
                 *out = s.p - s.q;
@@ -372,10 +396,10 @@ __device__ __forceinline__ Sums sweep(const RowView<T>& P, const RowView<T>& Q, 
         }
     }
     const int last = P.chunks() - 1;
-    if (last >= P.hi() && last >= k0 && last < k1 && last >= P.lo() && (last - k0) % 32 == lane) {  // and last one
+    if (last >= P.end() && last >= k0 && last < k1 && (last - k0) % 32 == lane) {  // the end of the tensor
         const u64 before = s.p - s.q;
-        const uint4 x = P.edge(last);
-        s.template take<T, KIND>(x, KIND != 0 ? Q.edge(last) : x, c);
+        const uint4 x = P.tail();
+        s.template take<T, KIND>(x, KIND != 0 ? Q.tail() : x, c);
         for (int i = (last - k0) / 32 / seg; i <= (its - 1) / seg; ++i) cum[i][threadIdx.x] += s.p - s.q - before;
     }
     return s;
@@ -523,8 +547,9 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
             const u64 out = sh.gone;
             const int node = sh.node;
             const int skew = static_cast<int>(((at + node) * a.V) % N);
-            const RowView<T> P{target + static_cast<size_t>(node) * a.V, skew, a.V};
-            const RowView<T> Q{draft + (draft != nullptr ? static_cast<size_t>(node) * a.V : 0), skew, a.V};
+            const bool open_end = at + node + 1 < static_cast<size_t>(a.B) * a.n;
+            const RowView<T> P{target + static_cast<size_t>(node) * a.V, skew, a.V, open_end};
+            const RowView<T> Q{draft + (draft != nullptr ? static_cast<size_t>(node) * a.V : 0), skew, a.V, open_end};
             const int per_piece = (P.chunks() + pieces - 1) >> (cl_log + kWarpsLog), its = (per_piece + 31) >> 5;
             const int seg = (its + kSegments - 1) / kSegments;
             const int k0 = min(piece * per_piece, P.chunks()), k1 = min(k0 + per_piece, P.chunks());
