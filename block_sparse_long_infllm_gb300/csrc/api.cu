@@ -163,6 +163,7 @@ int blocks_per_score_cta(const Params& p) { return 2048 / p.block_size; }
 
 // ---- rotary positions, drafts
 constexpr int kMaxHeads = 1 << 14;
+constexpr int kMaxRows = 1 << 30;  // token rows of a rope call
 
 bool natural(const void* p, uintptr_t size) { return (reinterpret_cast<uintptr_t>(p) & (size - 1)) == 0; }
 
@@ -212,7 +213,8 @@ int check_rope(const infllmv2_rope_params* in, int d, infllmv2::RopeArgs* a) {
 
 // Sizes of a chunk call; fills its rows (0: nothing to do).
 int check_chunk(const int32_t* cu_q, int B, int Tq, int total_q, int Hq, int L_max, infllmv2::RopeArgs* a) {
-    if (B < 0 || Tq < 0 || total_q < 0 || L_max <= 0 || L_max > kMaxLen || Hq > kMaxHeads) return INFLLMV2_ERR_INVALID_ARG;
+    if (B < 0 || Tq < 0 || total_q < 0 || total_q > kMaxRows || L_max <= 0 || L_max > kMaxLen || Hq > kMaxHeads)
+        return INFLLMV2_ERR_INVALID_ARG;
     a->rows = 0;
     if (B == 0 || Tq == 0) return INFLLMV2_OK;
     if (Tq > L_max) return INFLLMV2_ERR_INVALID_ARG;
@@ -845,7 +847,7 @@ int infllmv2_rope(const void* q, int64_t ld_q, const void* k, int64_t ld_k, cons
     infllmv2::RopeArgs a{};
     if (int rc = check_rope(rope, d, &a)) return rc;
     if (dtype != INFLLMV2_BF16 && dtype != INFLLMV2_FP32) return INFLLMV2_ERR_UNSUPPORTED;
-    if (rows < 0 || Hq <= 0 || Hk < 0 || Hq > kMaxHeads || Hk > kMaxHeads) return INFLLMV2_ERR_INVALID_ARG;
+    if (rows < 0 || rows > kMaxRows || Hq <= 0 || Hk < 0 || Hq > kMaxHeads || Hk > kMaxHeads) return INFLLMV2_ERR_INVALID_ARG;
     if (rows == 0) return INFLLMV2_OK;
     const int es = dtype == INFLLMV2_FP32 ? 4 : 2;
     if (!pos || !freqs || !natural(pos, 4) || !natural(freqs, 8)) return INFLLMV2_ERR_INVALID_ARG;
@@ -954,7 +956,7 @@ int infllmv2_rope_drafts(const void* q, int64_t ld_q, const void* k_new, int64_t
     if (B < 0 || n_draft < 0 || Hq > kMaxHeads) return INFLLMV2_ERR_INVALID_ARG;
     if (n_draft > 64) return INFLLMV2_ERR_UNSUPPORTED;
     if (B == 0 || n_draft == 0) return INFLLMV2_OK;
-    if (static_cast<int64_t>(B) * n_draft > INT32_MAX) return INFLLMV2_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(B) * n_draft > kMaxRows) return INFLLMV2_ERR_INVALID_ARG;
     a.rows = B * n_draft;
     if (int rc = check_new_rows(q, ld_q, k_new, ld_k, v_new, ld_v, q_out, Hq, Hkv, d, &a)) return rc;
     if (!draft_k || !draft_v || !aligned16(draft_k) || !aligned16(draft_v)) return INFLLMV2_ERR_INVALID_ARG;

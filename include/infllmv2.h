@@ -412,7 +412,8 @@ int infllmv2_rope_freqs(int scaling, int rotary_dim, double base, double factor,
  *           gradient of the inputs from the gradient of the outputs.
  * k may be NULL with k_out NULL and Hk 0.  An output may be its input (the same
  * pointer and ld); any other overlap is refused (here and below: of row tensors
- * with each other; caches and draft buffers overlap nothing else).  d 64 or 128.
+ * with each other; caches and draft buffers overlap nothing else).  d 64 or 128;
+ * at most 2^30 rows and 2^14 heads.
  */
 int infllmv2_rope(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const int32_t* pos, const uint64_t* freqs,
                   int rows, int Hq, int Hk, int d, int dtype, int transposed, void* q_out, int64_t ld_qo, void* k_out,
@@ -483,7 +484,8 @@ int infllmv2_rope_drafts(const void* q, int64_t ld_q, const void* k_new, int64_t
  *   draft == NULL: x stands iff u[x] Z < w(x); otherwise Z loses w(x), w(x) = 0.
  * The first child that stands is the next node; where none does, the last token
  * is the first one whose running sum of w passes u[0] * (sum of w), or of p when
- * w has nothing left.  Decisions are taken in 64 bits, sums in units of 2^-62.
+ * w has nothing left.  Sums are exact, in units of 2^-62 (what of a probability
+ * lies below that is dropped); comparisons are exact.
  *   tokens    [B, n_draft] int32; a root's is not read
  *   tree_mask [B, n_draft], NULL: a chain (node i's parent is i - 1)
  *   n_nodes   [B] int32 in [0, n_draft], nodes in use (0: the sequence is idle);
@@ -497,8 +499,10 @@ int infllmv2_rope_drafts(const void* q, int64_t ld_q, const void* k_new, int64_t
  * kv_len_out may be kv_len; both NULL or neither).
  * Probabilities: NaN and values below 0 are read as 0, values above 1 as 1.
  * Device errors (masks that are no tree, a token outside [0, V), n_nodes out of
- * range, a row whose sum is 0 or above 2) set the error word; that sequence's
- * outputs are those of an idle one: n_path 0, -1 elsewhere, kv_len unchanged.
+ * range, a target row that had to be summed -- the last node's, or one with
+ * children left after a rejection -- with a sum above 2, or the last node's with
+ * a sum of 0) set the error word; that sequence's outputs are those of an idle
+ * one: n_path 0, -1 elsewhere, kv_len unchanged.
  * Needs no workspace.  n_draft <= 64, V <= 2^24.
  */
 int infllmv2_verify(const int32_t* tokens, const uint64_t* tree_mask, const int32_t* n_nodes, const void* target,

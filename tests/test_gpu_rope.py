@@ -50,7 +50,8 @@ def _status():
     (1, 1, 1, 64, 64, 0, "bf16"), (1, 32, 2, 128, 128, 0, "bf16"), (3, 32, 2, 128, 128, 1, "bf16"),
     (7, 5, 3, 64, 32, 0, "bf16"), (33, 2, 1, 64, 16, 1, "fp32"), (65, 16, 16, 128, 96, 0, "fp32"),
     (130, 4, 0, 128, 2, 0, "bf16"), (130, 3, 1, 128, 50, 1, "bf16"), (130, 3, 1, 64, 6, 0, "fp32"),
-    (700, 33, 1, 64, 64, 1, "fp32"), (1301, 3, 1, 128, 64, 0, "bf16"), (1301, 7, 2, 128, 126, 0, "fp32")])
+    (700, 33, 1, 64, 64, 1, "fp32"), (1301, 3, 1, 128, 64, 0, "bf16"), (1301, 7, 2, 128, 126, 0, "fp32"),
+    (2601, 2, 1, 64, 32, 1, "bf16"), (2601, 1, 1, 64, 64, 0, "fp32"), (4999, 1, 1, 128, 128, 0, "bf16")])
 @pytest.mark.parametrize("transposed", [False, True])
 def test_rope_matches_definition(cuda_lib, rows, Hq, Hk, d, rot, inter, dtype, transposed):
     torch = torch_mod()
@@ -154,7 +155,7 @@ def _chunk(rng, B, Tq, L_max, packed):
 
 CHUNKS = [(1, 1, 8, 1, 1, 64, 64, 0, False), (4, 1, 40, 32, 2, 128, 128, 0, False), (3, 37, 100, 4, 2, 64, 32, 1, False),
           (5, 70, 71, 16, 1, 128, 128, 1, True), (7, 301, 512, 2, 2, 64, 64, 0, True), (2, 64, 64, 6, 3, 128, 30, 0, True),
-          (9, 5, 33, 8, 8, 64, 14, 1, True)]
+          (9, 5, 33, 8, 8, 64, 14, 1, True), (3, 1201, 1300, 1, 1, 64, 32, 0, True)]
 
 
 @pytest.mark.parametrize("B,Tq,L_max,Hq,Hkv,d,rot,inter,packed", CHUNKS)

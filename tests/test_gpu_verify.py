@@ -120,6 +120,45 @@ def test_chain_without_masks_and_many_sequences(cuda_lib):
     assert seen == {1, 2, 3, 4}
 
 
+@pytest.mark.parametrize("dtype,V", [("fp32", 33001), ("bf16", 33003), ("fp32", 16384)])
+@pytest.mark.parametrize("mode", ["replaced", "distinct", "fixed"])
+def test_every_batch_size_decides_alike(cuda_lib, dtype, V, mode):
+    """A sequence's row is spread over 16 CTAs when it is alone, 8 among 20, 4 among 100, one among 700: sums
+    are exact, so its outputs are the same; two of them against the exact rationals."""
+    torch = torch_mod()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V)
+    B, n = 6, 4
+    t = torch.float32 if dtype == "fp32" else torch.bfloat16
+    logits = torch.randn((B, n, V), generator=g, device="cuda") * 2.0
+    target = torch.softmax(logits, -1).to(t)
+    draft = torch.softmax(logits + torch.randn((B, n, V), generator=g, device="cuda"), -1)
+    tokens = torch.zeros((B, n), dtype=torch.int32, device="cuda")
+    tokens[:, 1:] = torch.multinomial(draft[:, 0], 3, replacement=mode == "replaced", generator=g).int()
+    draft = draft.to(t)
+    u = torch.rand((B, n), generator=g, device="cuda")
+    u[0, 1:], u[1, 1:] = 0.9999, 0.9999  # all three siblings are tried
+    parents = [-1, 0, 0, 0]
+    masks = to_dev(np.array([masks_of(parents)] * B, dtype=np.uint64))
+    outs = []
+    for copies in (1, 20, 100, 700):
+        for b in range(B):
+            rep = lambda x: x[b:b + 1].expand(copies, *x.shape[1:]).clone(memory_format=torch.contiguous_format)  # noqa: E731
+            out = _run(rep(tokens), rep(target), None if mode == "fixed" else rep(draft), rep(u), tree_mask=rep(masks),
+                       replace=mode != "distinct")
+            assert all(torch.equal(out[k], out[k][:1].expand_as(out[k])) for k in out)
+            outs.append({k: x[0].tolist() for k, x in out.items()})
+    assert lib().sync_status() == 0
+    for i in range(B, len(outs)):
+        assert outs[i] == outs[i % B]
+    for b in range(2):
+        path, toks = spec_ref.verify(tokens[b].tolist(), parents, target[b].double().cpu().numpy(),
+                                     None if mode == "fixed" else draft[b].double().cpu().numpy(), u[b].cpu().numpy(),
+                                     mode != "distinct")
+        assert outs[b]["path"][:len(path)] == path and outs[b]["out_tokens"][:len(toks)] == toks
+        assert outs[b]["n_path"] == len(path)
+
+
 def _one(target, draft, tokens, u, parents, **kw):
     """One sequence given as lists of rows."""
     n = len(tokens)

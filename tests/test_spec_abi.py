@@ -31,7 +31,8 @@ def rope_args(**kw):
     (dict(rope=rp(rotary_dim=0)), INV), (dict(rope=rp(rotary_dim=7)), INV), (dict(rope=rp(rotary_dim=130)), INV),
     (dict(rope=rp(interleaved=2)), INV), (dict(rope=rp(attn_scale=-1.0)), INV),
     (dict(rope=rp(attn_scale=float("nan"))), INV), (dict(rope=None), INV), (dict(d=96), UNS), (dict(dtype=2), UNS),
-    (dict(rows=-1), INV), (dict(Hq=0), INV), (dict(Hk=-1), INV), (dict(q=None), INV), (dict(pos=None), INV),
+    (dict(rows=-1), INV), (dict(rows=(1 << 30) + 1), INV), (dict(Hq=0), INV), (dict(Hk=-1), INV), (dict(q=None), INV),
+    (dict(pos=None), INV),
     (dict(freqs=None), INV), (dict(q_out=None), INV), (dict(k=None), INV), (dict(k_out=None), INV), (dict(Hk=0), INV),
     (dict(ld_q=4095), INV), (dict(ld_ko=255), INV), (dict(q=ctypes.c_void_p((1 << 32) + 8)), INV),
     (dict(freqs=ctypes.c_void_p((1 << 32) + 4)), INV),
@@ -56,7 +57,7 @@ def append_args(**kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(d=80), UNS), (dict(Hq=6, total=16), UNS), (dict(Hq=33), INV), (dict(Tq=65, total=130), INV),
-    (dict(total=17), INV), (dict(total=-1, cu=at(9)), INV), (dict(L_max=0), INV), (dict(L_max=(1 << 28) + 1), INV),
+    (dict(total=17), INV), (dict(total=-1, cu=at(9)), INV), (dict(total=(1 << 30) + 1, cu=at(9)), INV), (dict(L_max=0), INV), (dict(L_max=(1 << 28) + 1), INV),
     (dict(B=-1), INV), (dict(q=None), INV), (dict(k=None), INV), (dict(v=None), INV), (dict(q_out=None), INV),
     (dict(kc=None), INV), (dict(vc=None), INV), (dict(kv=None), INV), (dict(freqs=None), INV), (dict(ld_k=128), INV),
     (dict(q_out=at(1), ld_q=8192), INV), (dict(q_out=at(2)), INV), (dict(cu=ctypes.c_void_p((1 << 32) + 2)), INV),
