@@ -139,6 +139,21 @@ __device__ __forceinline__ void check_offsets(const RopeArgs& a) {
     if (bad) raise_error(a.err, kDevErrIndex);
 }
 
+// (cos, sin) of every pair of the CTA's T rows, times the scale.
+__device__ __forceinline__ void fill_table(const RopeArgs& a, int T, const Row* rows, float2* table) {
+    const int half = a.rot / 2, width = 32 - __clz(half - 1);  // 2^width places for the pairs of a row
+    for (int i = threadIdx.x; i < T << width; i += kRopeThreads) {
+        const int t = i >> width, pair = i & ((1 << width) - 1);
+        if (pair >= half) continue;
+        const unsigned long long turn =
+            a.freqs[pair] * static_cast<unsigned long long>(static_cast<long long>(rows[t].pos));
+        float sn, cs;
+        // the top 32 bits as a signed fraction of half a turn
+        sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &sn, &cs);
+        table[t * half + pair] = make_float2(cs * a.scale, (a.transposed ? -sn : sn) * a.scale);
+    }
+}
+
 // How a type's rows are spread: heads that a thread loads together, rows that a CTA takes at most, CTAs
 // per SM that the registers have to allow.  Measured on 4 x 16384 tokens of 32 + 2 + 2 heads of 128
 // (1.21 GB, 180 us at the copy rate) for bf16, us: heads 3, rows 8, 3 CTAs 175; 1, 4, 5: 190; 2, 8, 4:
@@ -213,15 +228,7 @@ __global__ void __launch_bounds__(kRopeThreads, Plan<Tin>::kResident) rope_kerne
     if constexpr (FORM == kRopeChunk || FORM == kRopeChunkBack)
         if (blockIdx.x == 0 && a.cu_q != nullptr) check_offsets(a);
     __syncthreads();
-    for (int i = tid; i < T * half; i += kRopeThreads) {
-        const int rr = i / half, pair = i % half;
-        const unsigned long long turn =
-            a.freqs[pair] * static_cast<unsigned long long>(static_cast<long long>(rows_s[rr].pos));
-        float sn, cs;
-        // the top 32 bits as a signed fraction of half a turn
-        sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &sn, &cs);
-        table[i] = make_float2(cs * a.scale, (a.transposed ? -sn : sn) * a.scale);
-    }
+    fill_table(a, T, rows_s, table);
     __syncthreads();
     const Row row = rows_s[t];
     if (!row.ok) return;
@@ -284,12 +291,112 @@ __global__ void __launch_bounds__(kRopeThreads, Plan<Tin>::kResident) rope_kerne
     }
 }
 
+// The same for rotated parts whose halves do not start on a vector's boundary (and neighbouring pairs
+// that end inside one): a thread takes one vector of a head, the heads' vectors are laid side by side in
+// the warp's shared memory, and each element finds its partner there.  (All lanes have read a head before
+// any writes it, so outputs may be inputs here too.)
+template <int FORM, typename Tin, typename Tout>
+__global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(RopeArgs a, int T) {
+    constexpr int VEC = 16 / sizeof(Tin), kHeads = 2;
+    constexpr bool kFromCache = FORM == kRopeChunkBack, kToCache = FORM == kRopeChunk || FORM == kRopeDrafts;
+    using VI = Vec<Tin, VEC>;
+    using VO = Vec<Tout, VEC>;
+    extern __shared__ float2 table[];  // [T][rot / 2] (cos, sin)
+    __shared__ Row rows_s[kRopeThreads];
+    __shared__ alignas(16) Tin side[kHeads][kRopeThreads * VEC];
+    const int tid = threadIdx.x, r0 = blockIdx.x * T, half = a.rot / 2;
+    pdl_wait();
+    pdl_trigger();
+    if (tid < T) rows_s[tid] = locate<FORM>(a, r0 + tid);
+    if constexpr (FORM == kRopeChunk || FORM == kRopeChunkBack)
+        if (blockIdx.x == 0 && a.cu_q != nullptr) check_offsets(a);
+    __syncthreads();
+    fill_table(a, T, rows_s, table);
+    __syncthreads();
+    const int J = a.d / VEC;                   // vectors of a head: 8, 16 or 32 lanes of a warp
+    const int per_row = kRopeThreads / J / T;  // heads of a row in flight
+    const int j = tid % J, slot = tid / J, t = slot / per_row;
+    const Row row = rows_s[t];
+    const int at = j * VEC;  // the vector's first element
+    // each element's partner (by its place in the head) and factors: y = x cos + partner sin
+    int partner[VEC];
+    float cs[VEC], sn[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        const int x = at + e;
+        const bool upper = a.interleaved ? (x & 1) != 0 : x >= half;
+        const int pair = a.interleaved ? x >> 1 : upper ? x - half : x;
+        partner[e] = x >= a.rot ? x : a.interleaved ? x ^ 1 : upper ? x - half : x + half;
+        const float2 w = x < a.rot && row.ok ? table[t * half + pair] : make_float2(1.f, 0.f);
+        cs[e] = w.x;
+        sn[e] = upper ? w.y : -w.y;
+    }
+    const long long r = r0 + t, per_head = static_cast<long long>(a.L_max) * a.d;
+    const int Hqk = a.Hq + a.Hk, heads = Hqk + a.Hv, first = slot % per_row;
+    const Tin* const q = static_cast<const Tin*>(a.q) + r * a.ld_q;
+    const Tin* const k = static_cast<const Tin*>(a.k) + (kFromCache ? row.cache : r * a.ld_k);
+    const Tin* const v = static_cast<const Tin*>(a.v) + (kFromCache ? row.cache : r * a.ld_v);
+    Tout* const qo = static_cast<Tout*>(a.q_out) + r * a.ld_qo;
+    Tout* const ko = static_cast<Tout*>(a.k_out) + (kToCache ? row.cache : r * a.ld_ko);
+    Tout* const vo = static_cast<Tout*>(a.v_out) + (kToCache ? row.cache : r * a.ld_vo);
+    for (int base = 0; base < heads; base += kHeads * per_row) {  // alike for every lane of a warp
+        VI A[kHeads];
+#pragma unroll
+        for (int u = 0; u < kHeads; ++u) {
+            const int h = base + first + u * per_row;
+            if (!row.ok || h >= heads) continue;
+            const bool is_q = h < a.Hq, is_k = h < Hqk;
+            const Tin* src = is_q ? q : is_k ? k : v;
+            src += (is_q ? h : is_k ? h - a.Hq : h - Hqk) * (kFromCache && !is_q ? per_head : a.d);
+            A[u].load(src + at);
+        }
+        __syncwarp();  // the last heads' partners were read
+#pragma unroll
+        for (int u = 0; u < kHeads; ++u) A[u].store(&side[u][tid * VEC]);
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < kHeads; ++u) {
+            const int h = base + first + u * per_row;
+            if (!row.ok || h >= heads) continue;
+            const bool is_q = h < a.Hq, is_k = h < Hqk;
+            Tout* dst = is_q ? qo : is_k ? ko : vo;
+            dst += (is_q ? h : is_k ? h - a.Hq : h - Hqk) * (kToCache && !is_q ? per_head : a.d);
+            VO Y = convert<Tin, Tout, VEC>(A[u]);
+            if (is_k && at < a.rot) {
+                const Tin* const head = &side[u][(tid - j) * VEC];
+                float y[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    Vec<Tin, 1> o;
+                    o.load(head + partner[e]);
+                    y[e] = A[u].get(e) * cs[e] + o.get(0) * sn[e];
+                }
+                VO turned;
+                turned.set(y);
+                // what lies behind the rotated part stays bit for bit (rot is even: whole words of bf16)
+                constexpr int kPerWord = sizeof(Tout) == 4 ? 1 : 2;
+#pragma unroll
+                for (int w = 0; w < VEC / kPerWord; ++w)
+                    if (at + w * kPerWord < a.rot) Y.m.w[w] = turned.m.w[w];
+            }
+            Y.store(dst + at);
+        }
+    }
+}
+
+// Rows that a CTA takes: up to `most`, more where a row has too few heads to occupy its threads, fewer
+// where that leaves SMs without work.
+int rows_per_cta(const RopeArgs& a, int slots, int most, int heads_at_once) {
+    const int heads = a.Hq + a.Hk + a.Hv;
+    int T = slots < most ? slots : most;
+    while (T < slots && slots / T * heads_at_once > heads) T *= 2;
+    while (T > 1 && a.rows < T * 2 * kSms) T /= 2;
+    return T;
+}
+
 template <int FORM, typename Tin, typename Tout, int VEC>
 cudaError_t launch(const RopeArgs& a) {
-    // rows a CTA takes: fewer where that leaves SMs without work
-    const int slots = kRopeThreads / (a.d / (2 * VEC));
-    int T = slots < Plan<Tin>::kRows ? slots : Plan<Tin>::kRows;
-    while (T > 1 && a.rows < T * 2 * kSms) T /= 2;
+    const int T = rows_per_cta(a, kRopeThreads / (a.d / (2 * VEC)), Plan<Tin>::kRows, Plan<Tin>::kHeads);
     const int grid = (a.rows - 1) / T + 1;
     const size_t smem = static_cast<size_t>(T) * (a.rot / 2) * sizeof(float2);
     // Loading before the row is located shortens a call of few CTAs (4 rows 2.34 -> 2.03 us, 16 drafts 2.8
@@ -299,14 +406,22 @@ cudaError_t launch(const RopeArgs& a) {
                          dim3(grid), dim3(kRopeThreads), smem, a.stream, true, a, T);
 }
 
-// Vectors of 16 bytes where both halves of the rotated part and every row start on a vector's
-// boundary, else single elements.
+template <int FORM, typename Tin, typename Tout>
+cudaError_t launch_any(const RopeArgs& a) {
+    constexpr int VEC = 16 / sizeof(Tin);
+    const int T = rows_per_cta(a, kRopeThreads / (a.d / VEC), 4, 2);
+    return launch_kernel(rope_any_kernel<FORM, Tin, Tout>, dim3((a.rows - 1) / T + 1), dim3(kRopeThreads),
+                         static_cast<size_t>(T) * (a.rot / 2) * sizeof(float2), a.stream, true, a, T);
+}
+
+// Vectors of 16 bytes where every row starts on a vector's boundary, else single elements; the pairs
+// within two vectors of a thread where both halves of the rotated part start on one as well.
 template <int FORM, typename Tin, typename Tout>
 cudaError_t launch_vec(const RopeArgs& a) {
     constexpr int VEC = 16 / sizeof(Tin);
     const long long ld = a.ld_q | a.ld_k | a.ld_v | a.ld_qo | a.ld_ko | a.ld_vo;
-    if (a.rot % (2 * VEC) == 0 && ld % VEC == 0) return launch<FORM, Tin, Tout, VEC>(a);
-    return launch<FORM, Tin, Tout, 1>(a);
+    if (ld % VEC != 0) return launch<FORM, Tin, Tout, 1>(a);
+    return a.rot % (2 * VEC) == 0 ? launch<FORM, Tin, Tout, VEC>(a) : launch_any<FORM, Tin, Tout>(a);
 }
 
 }  // namespace

@@ -468,30 +468,38 @@ def rope(q, k, pos, q_out, k_out, freqs, rope, transposed: bool = False, stream=
     """Rotary positions of q [rows, Hq, d] and k [rows, Hk, d] (None: q alone), bf16 or fp32, at
     positions pos [rows] int32, to q_out and k_out (which may be q and k).  transposed: the
     gradient of the inputs from that of the outputs.  Rows may be slices of a fused projection."""
-    _check(_binding().rope(q, k, pos, q_out, k_out, freqs, rope, transposed, stream), "infllmv2_rope")
+    rc = (_native or _binding()).rope(q, k, pos, q_out, k_out, freqs, rope, transposed, stream)
+    if rc != OK:
+        raise InfLLMv2Error(rc, "infllmv2_rope")
 
 
 def rope_append(q, k_new, v_new, q_out, k_cache, v_cache, kv_len, freqs, rope, cu_q=None, Tq_max=None, stream=None):
     """A chunk into the caches: q rotated to q_out, K rotated and V copied into rows kv_len - len .. of
     k_cache, v_cache [B, Hkv, L_max, d].  q, k_new, v_new [B, Tq, heads, d], or packed
     [total_q, heads, d] with cu_q and Tq_max; they may be slices of a fused projection."""
-    _check(_binding().rope_append(q, k_new, v_new, q_out, k_cache, v_cache, kv_len, freqs, rope, cu_q, Tq_max, stream),
-           "infllmv2_rope_append")
+    rc = (_native or _binding()).rope_append(q, k_new, v_new, q_out, k_cache, v_cache, kv_len, freqs, rope, cu_q,
+                                             Tq_max, stream)
+    if rc != OK:
+        raise InfLLMv2Error(rc, "infllmv2_rope_append")
 
 
 def rope_append_bwd(dq, dk, dv, dq_out, dk_out, dv_out, kv_len, freqs, rope, cu_q=None, Tq_max=None, stream=None):
     """The gradient of rope_append: from dq (of the rotated q) and dk, dv [B, Hkv, L_max, d] (of the
     caches), fp32 as sparse_attn_bwd gives them, those of the chunk's rows before rotation, bf16 or
     fp32.  The outputs may be slices of a fused gradient; dq_out may be dq."""
-    _check(_binding().rope_append_bwd(dq, dk, dv, dq_out, dk_out, dv_out, kv_len, freqs, rope, cu_q, Tq_max, stream),
-           "infllmv2_rope_append_bwd")
+    rc = (_native or _binding()).rope_append_bwd(dq, dk, dv, dq_out, dk_out, dv_out, kv_len, freqs, rope, cu_q,
+                                                 Tq_max, stream)
+    if rc != OK:
+        raise InfLLMv2Error(rc, "infllmv2_rope_append_bwd")
 
 
 def rope_drafts(q, k_new, v_new, q_out, draft_k, draft_v, kv_len, tree_mask, freqs, rope, stream=None):
     """A draft tree's rows [B, n_draft, heads, d] as decode takes them: q rotated to q_out, K rotated
     and V copied to draft_k, draft_v [B, Hkv, n_draft, d]; draft i at kv_len + its depth - 1."""
-    _check(_binding().rope_drafts(q, k_new, v_new, q_out, draft_k, draft_v, kv_len, tree_mask, freqs, rope, stream),
-           "infllmv2_rope_drafts")
+    rc = (_native or _binding()).rope_drafts(q, k_new, v_new, q_out, draft_k, draft_v, kv_len, tree_mask, freqs,
+                                             rope, stream)
+    if rc != OK:
+        raise InfLLMv2Error(rc, "infllmv2_rope_drafts")
 
 
 def verify(tokens, target, draft, u, path, n_path, out_tokens, tree_mask=None, n_nodes=None, kv_len=None,
@@ -501,12 +509,17 @@ def verify(tokens, target, draft, u, path, n_path, out_tokens, tree_mask=None, n
     probabilities draft [B, n, V] they were drawn from (None: they were chosen) and the numbers
     u [B, n] in [0, 1).  tree_mask None: a chain.  path, out_tokens [B, n], n_path [B] and, with
     kv_len, kv_len_out [B] (which may be kv_len) receive the result."""
-    _check(_binding().verify(tokens, target, draft, u, path, n_path, out_tokens, tree_mask, n_nodes, kv_len, kv_len_out,
-                             replace, stream), "infllmv2_verify")
+    rc = (_native or _binding()).verify(tokens, target, draft, u, path, n_path, out_tokens, tree_mask, n_nodes,
+                                        kv_len, kv_len_out,
+                                        replace, stream)
+    if rc != OK:
+        raise InfLLMv2Error(rc, "infllmv2_verify")
 
 
 def commit(draft_k, draft_v, path, n_path, k_cache, v_cache, kernel_cache, kv_len, params, stream=None):
     """The path's drafts become the last n_path tokens of the caches (kv_len counts them), and the
     semantic kernels they complete are pooled."""
-    _check(_binding().commit(draft_k, draft_v, path, n_path, k_cache, v_cache, kernel_cache, kv_len, params, stream),
-           "infllmv2_commit")
+    rc = (_native or _binding()).commit(draft_k, draft_v, path, n_path, k_cache, v_cache, kernel_cache, kv_len,
+                                        params, stream)
+    if rc != OK:
+        raise InfLLMv2Error(rc, "infllmv2_commit")

@@ -107,17 +107,39 @@ def test_rope_in_place_on_a_fused_projection(cuda_lib, rot):
     assert torch.equal(x[:, Hq + Hkv:], before[:, Hq + Hkv:])
 
 
-def test_rope_keeps_what_it_copies_bit_for_bit(cuda_lib):
+@pytest.mark.parametrize("rot", [64, 20])
+@pytest.mark.parametrize("inter", [0, 1])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rope_takes_rows_off_a_vectors_boundary(cuda_lib, rot, inter, dtype):
+    """Row strides that are no multiple of 16 bytes."""
+    torch = torch_mod()
+    rng = np.random.default_rng(rot)
+    rows, H, d, t = 37, 3, 64, _dt(dtype)
+    ld = H * d + (3 if dtype == "bf16" else 1)
+    x = _rand(rng, (rows, ld), t)
+    q = x[:, :H * d].unflatten(1, (H, d))
+    before = x.clone()
+    pos = np.arange(rows, dtype=np.int32) * 77
+    dev, table, _ = _freqs(rot)
+    lib().rope(q, None, torch.from_numpy(pos).cuda(), q, None, dev, dict(rotary_dim=rot, interleaved=inter))
+    assert _status() == 0
+    ref, amp = rotate(_np(before[:, :H * d].unflatten(1, (H, d))), turn_fraction(table, pos), rot, bool(inter))
+    _close(q, ref, amp, HALF[dtype], "odd strides")
+    assert torch.equal(x[:, H * d:], before[:, H * d:])
+
+
+@pytest.mark.parametrize("rot,inter", [(16, 0), (10, 0), (10, 1), (2, 0)])
+def test_rope_keeps_what_it_copies_bit_for_bit(cuda_lib, rot, inter):
     """NaN payloads and infinities behind the rotated part."""
     torch = torch_mod()
     bits = torch.arange(-32768, 32768, 1, dtype=torch.int32).to(torch.int16).cuda()  # every 16-bit pattern
     q = bits.view(-1, 1, 64).view(torch.bfloat16).clone()
     out = torch.zeros_like(q)
-    dev, _, _ = _freqs(16)
+    dev, _, _ = _freqs(rot)
     pos = torch.zeros(q.shape[0], dtype=torch.int32, device="cuda")
-    lib().rope(q, None, pos, out, None, dev, dict(rotary_dim=16))
+    lib().rope(q, None, pos, out, None, dev, dict(rotary_dim=rot, interleaved=inter))
     assert _status() == 0
-    assert torch.equal(out.view(torch.int16)[..., 16:], q.view(torch.int16)[..., 16:])
+    assert torch.equal(out.view(torch.int16)[..., rot:], q.view(torch.int16)[..., rot:])
 
 
 def test_rope_transposed_is_the_gradient(cuda_lib):
