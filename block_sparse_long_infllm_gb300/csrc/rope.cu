@@ -384,8 +384,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(RopeArgs a, int 
     }
 }
 
-// Rows that a CTA takes: up to `most`, more where a row has too few heads to occupy its threads, fewer
-// where that leaves SMs without work.
+// Rows that a CTA takes: up to `most`, more where a row has too few heads to occupy its threads (64K rows
+// of 3 heads: 32 rows 28 us, 8 rows 57), fewer where that leaves SMs without work.
 int rows_per_cta(const RopeArgs& a, int slots, int most, int heads_at_once) {
     const int heads = a.Hq + a.Hk + a.Hv;
     int T = slots < most ? slots : most;
@@ -400,8 +400,10 @@ cudaError_t launch(const RopeArgs& a) {
     const int grid = (a.rows - 1) / T + 1;
     const size_t smem = static_cast<size_t>(T) * (a.rot / 2) * sizeof(float2);
     // Loading before the row is located shortens a call of few CTAs (4 rows 2.34 -> 2.03 us, 16 drafts 2.8
-    // -> 2.5) but costs the larger ones, where other CTAs fill the wait (16384-token prompts 175 -> 198 us).
-    const bool early = grid <= 2 * kSms;
+    // -> 2.5), and one whose threads load no further heads (64K rows of 3 heads 28.1 -> 26.8), but costs the
+    // larger ones, where other CTAs fill the wait (16384-token prompts 175 -> 198 us).
+    const int per_row = kRopeThreads / (a.d / (2 * VEC)) / T;
+    const bool early = grid <= 2 * kSms || a.Hq + a.Hk + a.Hv <= Plan<Tin>::kHeads * per_row;
     return launch_kernel(early ? rope_kernel<FORM, Tin, Tout, VEC, true> : rope_kernel<FORM, Tin, Tout, VEC, false>,
                          dim3(grid), dim3(kRopeThreads), smem, a.stream, true, a, T);
 }
@@ -415,7 +417,9 @@ cudaError_t launch_any(const RopeArgs& a) {
 }
 
 // Vectors of 16 bytes where every row starts on a vector's boundary, else single elements; the pairs
-// within two vectors of a thread where both halves of the rotated part start on one as well.
+// within two vectors of a thread where both halves of the rotated part start on one as well (packed
+// prompts of 36 heads, us: 64 of 128 elements turned 41, 50 of them by rope_any_kernel 53 and by single
+// elements 85).
 template <int FORM, typename Tin, typename Tout>
 cudaError_t launch_vec(const RopeArgs& a) {
     constexpr int VEC = 16 / sizeof(Tin);
