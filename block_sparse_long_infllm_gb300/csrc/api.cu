@@ -815,6 +815,7 @@ int infllmv2_rope_freqs(int scaling, int rotary_dim, double base, double factor,
     }
     const double R = rotary_dim;
     if (scaling == INFLLMV2_ROPE_NTK) base *= pow(factor, R / (R - 2.0));
+    if (!(base > 0.0) || !isfinite(base)) return INFLLMV2_ERR_INVALID_ARG;  // a factor out of all range
     double low = 0.0, high = 0.0;  // pairs below low keep theta, pairs from high on get theta / factor
     if (scaling == INFLLMV2_ROPE_YARN) {
         low = fmax(floor(R * log(orig_len / (beta_fast * two_pi)) / (2.0 * log(base))), 0.0);
@@ -828,6 +829,7 @@ int infllmv2_rope_freqs(int scaling, int rotary_dim, double base, double factor,
             theta = theta / factor * ramp + theta * (1.0 - ramp);
         }
         if (scaling == INFLLMV2_ROPE_DIVISORS) theta /= divisors[i];
+        if (!isfinite(theta)) return INFLLMV2_ERR_INVALID_ARG;
         double whole;
         const double turns = modf(theta / two_pi, &whole);
         freqs_host[i] = static_cast<uint64_t>(ldexp(turns, 64));  // turns < 1: below 2^64

@@ -277,7 +277,7 @@ struct Shared {
     u64 rem;             // what is left of the target in piece `own`
     int node, own, state;
 };
-enum : int { kSweep = 0, kDraw = 1, kDone = 2, kBad = 3 };
+enum : int { kSweep = 0, kDraw = 1, kBad = 2 };
 
 __device__ __forceinline__ u64 warp_sum(u64 x) {
 #pragma unroll
@@ -685,6 +685,11 @@ cudaError_t launch(const VerifyArgs& a) {
     while (cl_log > 0 && ((static_cast<long long>(a.B) << cl_log) > kResident * 152 ||
                           a.V < (kVerifyThreads * RowView<T>::N) << cl_log))
         --cl_log;
+    if (cl_log > 3 &&  // past the portable size
+        cudaFuncSetAttribute(verify_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+        (void)cudaGetLastError();
+        cl_log = 3;
+    }
     const int CL = 1 << cl_log;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.B) * CL);
@@ -694,10 +699,6 @@ cudaError_t launch(const VerifyArgs& a) {
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = CL;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    if (CL > 8) {  // past the portable size
-        const cudaError_t e = cudaFuncSetAttribute(verify_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;

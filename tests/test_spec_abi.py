@@ -177,7 +177,8 @@ def test_freqs_scalings(built_lib):
     dict(rotary_dim=0), dict(rotary_dim=3), dict(base=1.0), dict(base=float("nan")), dict(scaling="linear", factor=0.0),
     dict(scaling="ntk", factor=float("inf")), dict(scaling="ntk", rotary_dim=2, factor=2.0),
     dict(scaling="yarn", factor=2.0, orig_len=0), dict(scaling="yarn", factor=2.0, orig_len=64, beta_slow=40.0),
-    dict(scaling="divisors", factor=2.0, orig_len=64),
+    dict(scaling="divisors", factor=2.0, orig_len=64), dict(scaling="ntk", factor=1e-320),
+    dict(scaling="ntk", factor=1e308), dict(scaling="linear", factor=1e-320),
     dict(scaling="divisors", factor=2.0, orig_len=64, rotary_dim=4, divisors=[1.0, 0.0]),
 ])
 def test_freqs_refuse(built_lib, kw):
