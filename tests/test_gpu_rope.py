@@ -384,3 +384,65 @@ def test_training_chunk_matches_fp64_autograd(cuda_lib):
         err, ref = np.abs(_np(got) - want.numpy()), np.abs(want.numpy())
         assert err.max() <= 2e-2 * ref.max(), f"d{name}: {err.max() / ref.max():.2e}"
         assert err.mean() <= 1e-2 * ref.mean(), f"d{name}: {err.mean() / ref.mean():.2e}"
+
+
+def test_caches_past_32_bits(cuda_lib):
+    """Caches of more than 2^32 elements, written and read back at their far end."""
+    torch = torch_mod()
+    rng = np.random.default_rng(2)
+    bf = torch.bfloat16
+    Hkv, d, T = 2, 128, 5
+    L = (1 << 24) + 40  # 2 heads of 2^31 elements and more
+    dev, table, _ = _freqs(128)
+    rp = dict(rotary_dim=128)
+    q, k, v = (_rand(rng, (1, T, h, d), bf) for h in (2, Hkv, Hkv))
+    kc = torch.zeros((1, Hkv, L, d), dtype=bf, device="cuda")
+    vc = torch.zeros((1, Hkv, L, d), dtype=bf, device="cuda")
+    kv = torch.tensor([L], dtype=torch.int32, device="cuda")
+    qo = torch.empty_like(q)
+    lib().rope_append(q, k, v, qo, kc, vc, kv, dev, rp)
+    assert _status() == 0
+    angle = turn_fraction(table, np.arange(L - T, L))
+    ref, amp = rotate(_np(k[0]), angle, 128, False)
+    _close(kc[0, :, L - T:].transpose(0, 1), ref, amp, HALF["bf16"], "k")
+    assert torch.equal(vc[0, :, L - T:].transpose(0, 1), v[0])
+    assert float(vc[0, 1, :T].abs().sum()) == 0.0  # what a wrapped offset would hit
+    # the commit of a path at the same end, over the rows just written
+    p = dict(block_size=64, kernel_size=32, kernel_stride=16, topk=4, n_init_blocks=1, n_local_blocks=2, dense_len=0)
+    kern = torch.zeros((1, Hkv, (L - 32) // 16 + 1, d), dtype=bf, device="cuda")
+    dk, dv = _rand(rng, (1, Hkv, 8, d), bf), _rand(rng, (1, Hkv, 8, d), bf)
+    path = torch.tensor([[1, 3, 4, 7, -1, -1, -1, -1]], dtype=torch.int32, device="cuda")
+    lib().commit(dk, dv, path, torch.tensor([4], dtype=torch.int32, device="cuda"), kc, vc, kern, kv, p)
+    assert _status() == 0
+    assert torch.equal(kc[0, :, L - 4:], dk[0, :, [1, 3, 4, 7]]) and torch.equal(vc[0, :, L - 4:], dv[0, :, [1, 3, 4, 7]])
+    del vc, kern
+    # gradients out of caches of the same size
+    g = torch.zeros((1, Hkv, L, d), dtype=torch.float32, device="cuda")
+    g[0, :, L - T:] = kc[0, :, L - T:].float()
+    outs = [torch.empty((1, T, h, d), device="cuda") for h in (2, Hkv, Hkv)]
+    lib().rope_append_bwd(torch.zeros((1, T, 2, d), device="cuda"), g, g, *outs, kv, dev, rp)
+    assert _status() == 0
+    ref, amp = rotate(_np(g[0, :, L - T:].transpose(0, 1)), angle, 128, False, 1.0, True)
+    _close(outs[1][0], ref, amp, HALF["fp32"], "dk")
+    assert torch.equal(outs[2][0], g[0, :, L - T:].transpose(0, 1))
+
+
+def test_rope_on_a_given_stream(cuda_lib):
+    """The stream as an object and as a handle, and the current one."""
+    torch = torch_mod()
+    rng = np.random.default_rng(4)
+    q = _rand(rng, (64, 4, 64), torch.bfloat16)
+    pos = torch.arange(64, dtype=torch.int32, device="cuda")
+    dev, _, _ = _freqs(64)
+    want = torch.empty_like(q)
+    lib().rope(q, None, pos, want, None, dev, dict(rotary_dim=64))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream, None):
+        out = torch.zeros_like(q)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s if stream is None else torch.cuda.current_stream()):
+            lib().rope(q, None, pos, out, None, dev, dict(rotary_dim=64), stream=stream)
+        s.synchronize()
+        assert torch.equal(out, want)
+    assert _status() == 0

@@ -269,6 +269,26 @@ def test_verify_keeps_the_targets_distribution(cuda_lib, mode):
     assert 0.2 < float((out["n_path"] == 2).double().mean()) < 1.0
 
 
+def test_verify_past_32_bits(cuda_lib):
+    """Probabilities of more than 2^32 elements: 65 chains of 64 over 2^20 tokens, each 2^-20."""
+    torch = torch_mod()
+    B, n, V = 65, 64, 1 << 20
+    target = torch.full((B, n, V), 2.0 ** -20, dtype=torch.bfloat16, device="cuda")
+    tokens = torch.arange(B * n, dtype=torch.int32, device="cuda").view(B, n) * 200 % V
+    u = torch.zeros((B, n), device="cuda")        # every draft stands
+    u[:, 0] = torch.arange(B, device="cuda") / B  # and the last token is V b / B
+    u[B - 1, n - 1] = 2.0 ** -20                   # but the last sequence's last: u = p is a rejection
+    out = _run(tokens, target, None, u)
+    assert lib().sync_status() == 0
+    last = (u[:, 0].double() * V).long()
+    for b in (0, 1, 37, B - 2):
+        _check(out, b, n, list(range(n)), tokens[b, 1:].tolist() + [last[b].item()])
+    # the rejected token weighs nothing: of the other V - 1, equally likely, that of u
+    at = int(u[B - 1, 0].double().item() * (V - 1))
+    at += at >= tokens[B - 1, n - 1].item()
+    _check(out, B - 1, n, list(range(n - 1)), tokens[B - 1, 1:n - 1].tolist() + [at])
+
+
 def test_verify_on_a_captured_graph_and_another_stream(cuda_lib):
     """Two captured graphs on two streams at once, replayed with new numbers, against eager calls."""
     torch = torch_mod()
