@@ -14,10 +14,10 @@
 
 #include <string.h>
 
+#include <new>
 #include <sstream>
 #include <stdexcept>
 #include <string>
-#include <vector>
 
 #include "infllmv2.h"
 
@@ -36,18 +36,19 @@ struct Bad : std::runtime_error {  // becomes a ValueError
 struct Call {
     c10::Device dev{c10::DeviceType::CPU};
     bool seen = false;
-    std::vector<const at::Tensor*> all;
+    const at::Tensor* all[16];
+    int count = 0;
 
     const at::Tensor& tensor(PyObject* o, const char* name) {
         if (!THPVariable_Check(o)) bad(std::string(name) + " must be a tensor");
         const at::Tensor& t = THPVariable_Unpack(o);
-        all.push_back(&t);
+        all[count++] = &t;  // at most 12 of a call
         return t;
     }
     const at::Tensor* maybe(PyObject* o, const char* name) { return o == Py_None ? nullptr : &tensor(o, name); }
     void place() {  // after the checks of types and shapes
-        for (const at::Tensor* t : all) {
-            const c10::Device d = t->device();
+        for (int i = 0; i < count; ++i) {
+            const c10::Device d = all[i]->device();
             if (!seen) {
                 if (!d.is_cuda()) bad("tensor must live on a CUDA device");
                 dev = d;
@@ -118,10 +119,34 @@ bool from_buffer(PyObject* o, P* p) {
     if (!fits) bad("not a parameter structure of this call");
     return true;
 }
-PyObject* field(PyObject* o, const char* name, bool needed) {  // new reference, or nullptr
-    PyObject* key = PyUnicode_FromString(name);
+// The names of the fields, made once.
+struct Names {
+    PyObject* key[11];
+    Names() {
+        const char* const text[11] = {"rotary_dim", "interleaved", "attn_scale", "block_size", "kernel_size", "kernel_stride",
+                                      "topk", "n_init_blocks", "n_local_blocks", "dense_len", "softmax_scale"};
+        for (int i = 0; i < 11; ++i) key[i] = PyUnicode_InternFromString(text[i]);
+    }
+};
+enum : int {
+    kRotaryDim, kInterleaved, kAttnScale, kBlockSize, kKernelSize, kKernelStride, kTopk, kNInit, kNLocal, kDenseLen,
+    kSoftmaxScale
+};
+PyObject* field(PyObject* o, int which, bool needed) {  // new reference, or nullptr
+    static const Names names;
+    PyObject* const key = names.key[which];
+    if (key == nullptr) throw std::bad_alloc();
+    if (PyDict_CheckExact(o)) {
+        PyObject* v = PyDict_GetItemWithError(o, key);
+        if (v != nullptr) return Py_NewRef(v);
+        if (PyErr_Occurred()) throw std::runtime_error("");
+        if (needed) {
+            PyErr_SetObject(PyExc_KeyError, key);
+            throw std::runtime_error("");
+        }
+        return nullptr;
+    }
     PyObject* v = PyObject_GetItem(o, key);
-    Py_DECREF(key);
     if (v == nullptr) {
         if (needed || !PyErr_ExceptionMatches(PyExc_KeyError)) throw std::runtime_error("");
         PyErr_Clear();
@@ -129,19 +154,19 @@ PyObject* field(PyObject* o, const char* name, bool needed) {  // new reference,
     return v;
 }
 // A field as Python's int() and float() take it.
-int32_t int_field(PyObject* o, const char* name, bool needed = true) {
-    PyObject* v = field(o, name, needed);
+int32_t int_field(PyObject* o, int which, bool needed = true) {
+    PyObject* v = field(o, which, needed);
     if (v == nullptr) return 0;
-    PyObject* i = PyNumber_Long(v);
+    PyObject* i = PyLong_CheckExact(v) ? Py_NewRef(v) : PyNumber_Long(v);
     Py_DECREF(v);
     if (i == nullptr) throw std::runtime_error("");
     const int64_t x = PyLong_AsLongLong(i);
     Py_DECREF(i);
     if (x == -1 && PyErr_Occurred()) throw std::runtime_error("");
-    return as_int(x, name);
+    return as_int(x, "a parameter");
 }
-float float_field(PyObject* o, const char* name) {
-    PyObject* v = field(o, name, false);
+float float_field(PyObject* o, int which) {
+    PyObject* v = field(o, which, false);
     if (v == nullptr) return 0.f;
     const double x = PyFloat_AsDouble(v);
     Py_DECREF(v);
@@ -151,22 +176,22 @@ float float_field(PyObject* o, const char* name) {
 infllmv2_rope_params rope_params(PyObject* o) {
     infllmv2_rope_params p;
     if (from_buffer(o, &p)) return p;
-    p.rotary_dim = int_field(o, "rotary_dim");
-    p.interleaved = int_field(o, "interleaved", false);
-    p.attn_scale = float_field(o, "attn_scale");
+    p.rotary_dim = int_field(o, kRotaryDim);
+    p.interleaved = int_field(o, kInterleaved, false);
+    p.attn_scale = float_field(o, kAttnScale);
     return p;
 }
 infllmv2_params method_params(PyObject* o) {
     infllmv2_params p;
     if (from_buffer(o, &p)) return p;
-    p.block_size = int_field(o, "block_size");
-    p.kernel_size = int_field(o, "kernel_size");
-    p.kernel_stride = int_field(o, "kernel_stride");
-    p.topk = int_field(o, "topk");
-    p.n_init_blocks = int_field(o, "n_init_blocks");
-    p.n_local_blocks = int_field(o, "n_local_blocks");
-    p.dense_len = int_field(o, "dense_len");
-    p.softmax_scale = float_field(o, "softmax_scale");
+    p.block_size = int_field(o, kBlockSize);
+    p.kernel_size = int_field(o, kKernelSize);
+    p.kernel_stride = int_field(o, kKernelStride);
+    p.topk = int_field(o, kTopk);
+    p.n_init_blocks = int_field(o, kNInit);
+    p.n_local_blocks = int_field(o, kNLocal);
+    p.dense_len = int_field(o, kDenseLen);
+    p.softmax_scale = float_field(o, kSoftmaxScale);
     return p;
 }
 
