@@ -252,6 +252,30 @@ def test_append_bwd_matches_definition(cuda_lib, B, Tq, L_max, Hq, Hkv, d, rot, 
         r += n[b]
 
 
+@pytest.mark.parametrize("rot", [64, 22])
+def test_append_bwd_leaves_other_rows_and_turns_in_place(cuda_lib, rot):
+    """dq_out is dq; rows of a sequence that is skipped and behind the last one keep what they held."""
+    torch = torch_mod()
+    rng = np.random.default_rng(rot)
+    n, L, H, d = [3, 4, 2], 16, 2, 64
+    kv = torch.tensor([3, 17, 9], dtype=torch.int32, device="cuda")  # the second is past the cache
+    rows = sum(n) + 2
+    dq = _rand(rng, (rows, H, d), torch.float32)
+    before = dq.clone()
+    dk, dv = _rand(rng, (3, 1, L, d), torch.float32), _rand(rng, (3, 1, L, d), torch.float32)
+    ko, vo = (torch.full((rows, 1, d), 7.0, device="cuda") for _ in range(2))
+    dev, table, _ = _freqs(rot)
+    cu = torch.tensor(np.cumsum([0] + n), dtype=torch.int32, device="cuda")
+    lib().rope_append_bwd(dq, dk, dv, dq, ko, vo, kv, dev, dict(rotary_dim=rot), cu_q=cu, Tq_max=4)
+    assert _status() == lib().ERR_DEVICE_INDEX
+    kept = [3, 4, 5, 6, 9, 10]
+    assert torch.equal(dq[kept], before[kept]) and bool((ko[kept] == 7.0).all()) and bool((vo[kept] == 7.0).all())
+    for sl, x in ((slice(0, 3), np.arange(0, 3)), (slice(7, 9), np.arange(7, 9))):
+        ref, amp = rotate(_np(before[sl]), turn_fraction(table, x), rot, False, 1.0, True)
+        _close(dq[sl], ref, amp, HALF["fp32"], "dq")
+    assert torch.equal(vo[7:9, 0], dv[2, 0, 7:9])
+
+
 def test_append_skips_bad_sequences_and_reports(cuda_lib):
     torch = torch_mod()
     bf = torch.bfloat16
