@@ -584,6 +584,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
                 if (!mbar_wait(&sh.bar[buf], (round >> 1) & 1)) {
                     if (lane == 0) raise_error(a.err, kDevErrTimeout);
                     state = kBad;
+                    (void)mbar_wait(&sh.bar[buf], (round >> 1) & 1);  // what is still on its way here may land
                 } else {
                     if (lane == 0) mbar_arrive_expect_tx(&sh.bar[buf], pieces * sizeof(Part));  // the round after the next
                     // a lane sums its pieces; a scan over the lanes orders them
