@@ -63,6 +63,9 @@ __device__ __forceinline__ u64 shr(u64 x, int n) {
     return y;
 }
 
+// max(a - b, 0).
+__device__ __forceinline__ u64 less(u64 a, u64 b) { return a > b ? a - b : 0ull; }
+
 // A probability as read: NaN and negative values are 0, values past 1 are 1.
 __device__ __forceinline__ float prob(float x) { return __saturatef(x); }
 
@@ -130,7 +133,7 @@ __device__ __forceinline__ u64 scaled(float q, const Num& c) {
 __device__ __forceinline__ u64 weight(float p, float q, const Coef& c) {
     const u64 P = add_fixed(0ull, p);
     const u64 Q = c.kind == 0 ? 0ull : c.kind == 1 ? add_fixed(0ull, q) : scaled(q, c.v);
-    return P > Q ? P - Q : 0ull;
+    return less(P, Q);
 }
 
 // u Z q < w R, exactly: u, q in [0, 1]; Z, w, R in units of 2^-62.  The 128-bit products are compared
@@ -470,7 +473,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
     if (!idle) {
         // the walk (warp 0)
         u64 on = 1ull, rest = 0ull, gone = 0ull, Z = kOne, easy = 0ull;
-        long long R = static_cast<long long>(kOne);
+        u64 R = kOne;  // what is left of the drafts' weight; 0 stays 0, however many siblings follow
         Coef c{{0ull, 0}, 0};
         int cur = 0;
         bool fresh = true, z_known = true;  // no child of cur was tried yet; Z belongs to c
@@ -506,11 +509,11 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
                         if (draft == nullptr) {
                             const u64 w = add_fixed(0ull, sh.p[i]);
                             gone = 1ull << i;
-                            Z = Z > w ? Z - w : 0ull;
+                            Z = less(Z, w);
                         } else {
                             c = Coef{{1ull << 63, 0}, 1};
                             z_known = false;
-                            if (!a.replace) R -= static_cast<long long>(add_fixed(0ull, sh.q[i]));
+                            if (!a.replace) R = less(R, add_fixed(0ull, sh.q[i]));
                         }
                         continue;
                     }
@@ -520,28 +523,28 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
                     u64 w = weight(sh.p[i], q, c);  // c = 0 without draft probabilities
                     for (u64 g = gone; g != 0ull; g &= g - 1)
                         if (sh.tok[lowest(g)] == sh.tok[i]) w = 0ull;
-                    if (R > 0 && stands(sh.u[i], Z, q, w, static_cast<u64>(R))) {
+                    if (R != 0ull && stands(sh.u[i], Z, q, w, R)) {
                         on |= 1ull << i;
                         gone = 0ull;
                         c.kind = 0;
                         Z = kOne;
-                        R = static_cast<long long>(kOne);
+                        R = kOne;
                         fresh = true;
                         continue;
                     }
                     rest &= rest - 1;
                     if (draft == nullptr) {
                         gone |= 1ull << i;
-                        Z = Z > w ? Z - w : 0ull;
+                        Z = less(Z, w);
                     } else {
-                        if (R > 0 && Z != 0ull) {
+                        if (R != 0ull && Z != 0ull) {
                             Num z = num(Z);
-                            if (R != static_cast<long long>(kOne)) z = divide(z, num(static_cast<u64>(R)));
+                            if (R != kOne) z = divide(z, num(R));
                             c.v = add(c.v, z);
                             c.kind = 2;  // past 1
                             z_known = false;
                         }
-                        if (!a.replace) R -= static_cast<long long>(add_fixed(0ull, q));
+                        if (!a.replace) R = less(R, add_fixed(0ull, q));
                     }
                 }
                 if (lane == 0) {

@@ -194,6 +194,24 @@ def test_verify_at_its_borders(cuda_lib):
     assert lib().sync_status() == 0
 
 
+def test_rejected_siblings_past_the_drafts_weight_change_nothing(cuda_lib):
+    """Without replacement R stays at nothing once the rejected siblings' q have used it up, however far
+    their sum goes past it: duplicates of a drafted token (sums from 2 to 62), and rows above 1."""
+    one, other = [1.0, 0.0, 0.0, 0.0], [0.0, 1.0, 0.0, 0.0]
+    for twins in range(2, 63):
+        n = twins + 2
+        tokens, parents, u = [0] * (n - 1) + [1], [-1] + [0] * (n - 1), [0.5] * n
+        want = spec_ref.verify(tokens, parents, [other] * n, [one] * n, u, False)
+        assert want == ([0], [1])
+        assert _one([other] * n, [one] * n, tokens, u, parents, replace=False) == want
+    big, p = [7.0, 0.75, 0.75, 0.0], [0.0, 0.25, 0.25, 0.5]  # 7 is read as 1
+    tokens, parents, u = [0, 0, 1, 2, 0, 3, 3], [-1] + [0] * 6, [0.5, 0.5, 0.9, 0.9, 0.5, 0.0, 0.5]
+    want = spec_ref.verify(tokens, parents, [p] * 7, [big] * 7, u, False)
+    assert want == ([0], [3])
+    assert _one([p] * 7, [big] * 7, tokens, u, parents, replace=False) == want
+    assert lib().sync_status() == 0
+
+
 def test_verify_reads_bad_numbers_as_documented(cuda_lib):
     nan, inf = float("nan"), float("inf")
     assert _one([[nan, 0.5, -1.0, 0.5]], None, [0], [0.0], [-1]) == ([0], [1])
