@@ -4,7 +4,8 @@
 // magnitude (exact for every value within 2^40 of the largest -- the condition under which an
 // fp64 sum of bf16 values is exact as well), the integers are added, and the quotient by c, with
 // its remainder as a sticky bit, is rounded once, nearest with ties to even.  (This GPU's fp64
-// rate is a few operations per clock per SM, so no fp64 is used.)
+// rate is a few operations per clock per SM, so no fp64 is used.)  Exponent 255 is no number of that
+// scale: a column with infinities of one sign has that mean, one with both or with a NaN is NaN.
 #pragma once
 
 #include "common.cuh"
@@ -53,6 +54,41 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t max_s16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// bf16 bits of the mean of column ln % 8 of a slice where it holds an infinity or a NaN, else 0.  Without
+// their sign the largest bits are a NaN's or an infinity's; where they are an infinity's, +inf is the
+// largest signed and -inf the largest unsigned pattern.
+template <int kRows>
+__device__ __forceinline__ uint32_t special_mean(const uint32_t (&w)[kRows][4], int ln) {
+    uint32_t out = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t mag = 0u, pos = 0x80008000u, neg = 0u;
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            mag = max_u16x2(mag, w[u][i] & 0x7FFF7FFFu);
+            pos = max_s16x2(pos, w[u][i]);
+            neg = max_u16x2(neg, w[u][i]);
+        }
+#pragma unroll
+        for (int off = 1; off < kMeanLanes; off <<= 1) {
+            mag = max_u16x2(mag, __shfl_xor_sync(0xffffffffu, mag, off));
+            pos = max_s16x2(pos, __shfl_xor_sync(0xffffffffu, pos, off));
+            neg = max_u16x2(neg, __shfl_xor_sync(0xffffffffu, neg, off));
+        }
+        const int sh = 16 * (ln & 1);
+        const uint32_t m = (mag >> sh) & 0xFFFFu, p = (pos >> sh) & 0xFFFFu, n = (neg >> sh) & 0xFFFFu;
+        if (i == (ln & 7) >> 1 && m >= 0x7F80u)
+            out = m > 0x7F80u || (p == 0x7F80u && n == 0xFF80u) ? 0x7FFFu : p == 0x7F80u ? p : n;
+    }
+    return out;
+}
+
 // Exact mean of the c rows of one 8-element slice; lane ln (of the 16 aligned lanes sharing the
 // slice) takes rows ln, ln + 16, ... (at most kRows of them) from row(i).  Every lane of the group
 // returns the 8 bf16 results, packed.
@@ -84,6 +120,9 @@ __device__ __forceinline__ uint4 exact_mean_rows(int c, int ln, RowOf row) {
     for (int off = 1; off < kMeanLanes; off <<= 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) xm2[i] = max_u16x2(xm2[i], __shfl_xor_sync(0xffffffffu, xm2[i], off));
+    const uint32_t top = max_u16x2(max_u16x2(xm2[0], xm2[1]), max_u16x2(xm2[2], xm2[3]));
+    uint32_t special = 0u;
+    if (__any_sync(0xffffffffu, (top >> 16) == 0x7F80u || (top & 0xFFFFu) == 0x7F80u)) special = special_mean<kRows>(w, ln);
     int emax[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) emax[e] = static_cast<int>((xm2[e >> 1] >> (16 * (e & 1) + 7)) & 0xFFu);
@@ -123,8 +162,8 @@ __device__ __forceinline__ uint4 exact_mean_rows(int c, int ln, RowOf row) {
     Sm += __shfl_xor_sync(0xffffffffu, Sm, 8);
     const uint32_t xw = (ln & 4) ? ((ln & 2) ? xm2[3] : xm2[2]) : ((ln & 2) ? xm2[1] : xm2[0]);
     const int xm = static_cast<int>((xw >> (16 * (ln & 1) + 7)) & 0xFFu);
-    const uint32_t bits =
-        bf16_of_ratio(static_cast<unsigned long long>(Sm < 0 ? -Sm : Sm), c, xm - 40 - 134, Sm < 0);
+    uint32_t bits = bf16_of_ratio(static_cast<unsigned long long>(Sm < 0 ? -Sm : Sm), c, xm - 40 - 134, Sm < 0);
+    if (special != 0u) bits = special;
     const int g0 = (threadIdx.x & 31) & ~(kMeanLanes - 1);  // first lane of this group in the warp
     uint32_t out[4];
 #pragma unroll

@@ -134,6 +134,9 @@ size_t infllmv2_workspace_size(int entry, int B, int Tq, int Hq, int Hkv, int d,
  * a new kernel completes every `stride` tokens).  Sums are exact -- integer
  * fixed-point sums of the bf16 inputs under a shared per-column exponent -- and
  * the mean is rounded to bf16 once, nearest-even.
+ * (Terms more than 2^40 below a column's largest lose their bits below that.)  A
+ * column with infinities of one sign has that infinity as its mean; with both, or
+ * with a NaN, its mean is NaN.
  * Requires 0 <= tok_begin <= tok_end <= L_max and
  * M_max >= (tok_end - kernel_size)/kernel_stride + 1.  Other kernels are untouched.
  */
