@@ -14,6 +14,7 @@
 // The launches carry programmatic stream serialisation, so a call's start-up overlaps the tail of the one
 // before (0.3 to 0.5 us of a small call).
 #include "internal.h"
+#include "places.h"
 
 namespace infllmv2 {
 
@@ -105,16 +106,12 @@ __device__ __forceinline__ Row locate(const RopeArgs& a, int r) {
             t = r % a.Tq;
             len = a.Tq;
         } else {
-            int lo = 0, hi = a.B;  // the last b with cu[b] <= r
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (a.cu_q[mid] <= r) lo = mid; else hi = mid;
-            }
-            b = lo;
-            t = r - a.cu_q[b];
-            len = a.cu_q[b + 1] - a.cu_q[b];
-            // a bad length is reported by check_offsets; rows behind the last sequence are left as they are
-            if (t < 0 || t >= len || len > a.Tq) return w;
+            // bad offsets are reported by check_offsets; rows behind the last sequence are left as they are
+            const PackedRow p = packed_row(a.cu_q, a.B, r, a.rows, a.Tq);
+            if (p.len == 0) return w;
+            b = p.b;
+            t = p.t;
+            len = p.len;
         }
         const int L = a.kv_len[b];
         if (L < len || L > a.L_max) {
@@ -132,7 +129,7 @@ __device__ __forceinline__ Row locate(const RopeArgs& a, int r) {
 __device__ __forceinline__ void check_offsets(const RopeArgs& a) {
     bool bad = false;
     for (int b = threadIdx.x; b < a.B; b += kRopeThreads) {
-        const int len = a.cu_q[b + 1] - a.cu_q[b];
+        const long long len = static_cast<long long>(a.cu_q[b + 1]) - a.cu_q[b];
         bad = bad || len < 0 || len > a.Tq;
     }
     if (threadIdx.x == 0) bad = bad || a.cu_q[0] != 0 || a.cu_q[a.B] > a.rows;

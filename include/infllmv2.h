@@ -434,8 +434,10 @@ int infllmv2_rope(const void* q, int64_t ld_q, const void* k, int64_t ld_k, cons
  * [total_q, Hq, d] packed, q itself when ld_q = Hq*d; caches [B, Hkv, L_max, d].
  * Kernels that the chunk completes are pooled by infllmv2_kernel_pool(_varlen).
  * Device errors (kv_len[b] below the chunk's length or past L_max, a length
- * outside [0, Tq], cu_q[B] past total_q) set the error word; that sequence is
- * skipped.
+ * outside [0, Tq], cu_q[0] not 0, cu_q[B] past total_q) set the error word.  A
+ * sequence is taken whole or skipped: those of such a length or kv_len, those
+ * that reach outside [0, total_q), and, of sequences that share rows (descending
+ * offsets), all or all but one.  Calls without work (B, Tq or total_q 0) read no offsets.
  */
 int infllmv2_rope_append(const void* q, int64_t ld_q, const void* k_new, int64_t ld_k, const void* v_new, int64_t ld_v,
                          void* q_out, void* k_cache, void* v_cache, const int32_t* kv_len, const int32_t* cu_q,

@@ -470,3 +470,39 @@ def test_rope_on_a_given_stream(cuda_lib):
         s.synchronize()
         assert torch.equal(out, want)
     assert _status() == 0
+
+
+@pytest.mark.parametrize("cu,taken", [([0, 4, 8], [True, False]), ([0, 4, 2, 6], [None, False, None]),
+                                      ([0, 2, 4, 3, 6], [True, None, False, None]), ([2, 4, 6], [True, True]),
+                                      ([-2, 2, 6], [False, True]), ([0, 3, 3, 2 ** 31 - 1], [True, False, False])])
+def test_packed_sequences_are_taken_whole_or_not_at_all(cuda_lib, cu, taken):
+    """Six rows under offsets that reach past them, descend or start elsewhere: a sequence's rows are all
+    written or all left as they were, forward and back, and the call reports.  (None: the sequence shares
+    rows with another one; at most one of them is taken.)"""
+    torch = torch_mod()
+    L, bf, B, d, room = lib(), torch.bfloat16, len(cu) - 1, 64, 16
+    rows = torch.ones((6, 1, d), dtype=bf, device="cuda")
+    kc, vc = (torch.zeros((B, 1, room, d), dtype=bf, device="cuda") for _ in range(2))
+    qo = torch.full_like(rows, 7.0)
+    kv = torch.full((B,), 10, dtype=torch.int32, device="cuda")
+    dev, _, _ = _freqs(64)
+    offsets = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    L.rope_append(rows, rows.clone(), rows.clone(), qo, kc, vc, kv, dev, dict(rotary_dim=64), cu_q=offsets, Tq_max=4)
+    assert _status() == L.ERR_DEVICE_INDEX
+    g = torch.ones((B, 1, room, d), device="cuda")
+    dq = torch.ones((6, 1, d), device="cuda")
+    outs = [torch.full((6, 1, d), 7.0, device="cuda") for _ in range(3)]
+    L.rope_append_bwd(dq, g, g.clone(), *outs, kv, dev, dict(rotary_dim=64), cu_q=offsets, Tq_max=4)
+    assert _status() == L.ERR_DEVICE_INDEX
+    written = []
+    for b in range(B):
+        n, cached = cu[b + 1] - cu[b], (vc[b, 0].float().sum(-1) > 0).tolist()
+        if taken[b] or (taken[b] is None and any(cached)):
+            assert cached == [10 - n <= x < 10 for x in range(room)], b
+            written += range(cu[b], cu[b + 1])
+        else:
+            assert not any(cached), b
+    assert len(written) == len(set(written))
+    for r in range(6):
+        assert bool((qo[r] == 7.0).all()) == (r not in written)
+        assert [bool((o[r] == 7.0).all()) for o in outs] == [r not in written] * 3
