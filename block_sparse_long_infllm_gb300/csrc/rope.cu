@@ -6,13 +6,15 @@
 //   y_a = s (a cos - b sin),  y_b = s (a sin + b cos)
 // and its transpose (the gradient) by the opposite angle; elements past rot are copied.  theta_i
 // comes as turns per position in units of 2^-64 (theta_i / 2 pi, fraction only): x times it, modulo
-// 2^64, is the exact fraction of a turn for any 32-bit position, so a far position loses nothing
-// (in fp32 the angle of position 10^6 would be off by up to 0.03 radians).
+// 2^64, is that many turns' fraction without a rounding for any 32-bit position, so an angle is as good as
+// the table, which is made in fp64 (in fp32 the angle of position 10^6 would be off by up to 0.03
+// radians).  angle.h takes cosine and sine of it.
 //
 // What bounds it is memory: every element is read once and written once.  4 prompts of 16384 tokens of
 // 32 + 2 + 2 heads of 128, bf16: 176 us, 6.85 TB/s; a decode step of 4 rows: 2.0 us, a launch's latency.
 // The launches carry programmatic stream serialisation, so a call's start-up overlaps the tail of the one
 // before (0.3 to 0.5 us of a small call).
+#include "angle.h"
 #include "internal.h"
 #include "places.h"
 
@@ -144,10 +146,9 @@ __device__ __forceinline__ void fill_table(const RopeArgs& a, int T, const Row* 
         if (pair >= half) continue;
         const unsigned long long turn =
             a.freqs[pair] * static_cast<unsigned long long>(static_cast<long long>(rows[t].pos));
-        float sn, cs;
-        // the top 32 bits as a signed fraction of half a turn
-        sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &sn, &cs);
-        table[t * half + pair] = make_float2(cs * a.scale, (a.transposed ? -sn : sn) * a.scale);
+        float cs, sn;
+        cos_sin_of_turn(turn, a.scale, &cs, &sn);
+        table[t * half + pair] = make_float2(cs, a.transposed ? -sn : sn);
     }
 }
 

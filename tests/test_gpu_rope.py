@@ -506,3 +506,53 @@ def test_packed_sequences_are_taken_whole_or_not_at_all(cuda_lib, cu, taken):
     for r in range(6):
         assert bool((qo[r] == 7.0).all()) == (r not in written)
         assert [bool((o[r] == 7.0).all()) for o in outs] == [r not in written] * 3
+
+
+@pytest.mark.parametrize("scaling", ["plain", "yarn"])
+@pytest.mark.parametrize("inter", [0, 1])
+def test_fp32_rows_lose_no_more_than_a_plain_fp32_rotation(cuda_lib, scaling, inter):
+    """The mean error of fp32 rows (a bound on the worst one cannot see an angle held in too few bits)
+    against fp64, beside that of factors rounded from fp64 and products and sums in fp32.  The kernel
+    takes one of two products and the sum without a rounding between, which is worth more than what its
+    factors lose: of about five roundings alike it has four and a twentieth."""
+    torch = torch_mod()
+    rng = np.random.default_rng(12 + inter)
+    rows, H, d = 4096, 8, 128
+    kw = dict(scaling="yarn", factor=8.0, orig_len=4096) if scaling == "yarn" else {}
+    dev, table, scale = _freqs(d, 10000.0, **kw)
+    scale = float(np.float32(scale))
+    rp = dict(rotary_dim=d, interleaved=inter, attn_scale=scale)
+    x = _rand(rng, (rows, H, d), torch.float32)
+    pos = rng.integers(0, 32768, rows).astype(np.int32)
+    turns = np.multiply.outer(pos.astype(np.int64).view(np.uint64), table)  # modulo 2^64
+    angle = torch.from_numpy((turns.astype(np.float64) / 2.0 ** 64 * 2.0 * np.pi)).cuda()[:, None]
+
+    def turn(x, c, s):
+        a, b = (x[..., 0::2], x[..., 1::2]) if inter else (x[..., :d // 2], x[..., d // 2:])
+        y = (a * c - b * s, a * s + b * c)
+        return torch.stack(y, -1).flatten(-2) if inter else torch.cat(y, -1)
+
+    def rms(y, ref):
+        return float((y.double() - ref).square().mean().sqrt())
+
+    for back in (False, True):
+        c, s = angle.cos() * scale, angle.sin() * scale * (-1.0 if back else 1.0)
+        ref, plain = turn(x.double(), c, s), turn(x, c.float(), s.float())
+        out = torch.empty_like(x)
+        lib().rope(x, None, torch.from_numpy(pos).cuda(), out, None, dev, rp, transposed=back)
+        assert _status() == 0
+        assert rms(out, ref) <= rms(plain, ref)
+    # and the gradient out of the caches
+    T = 2048
+    kv = torch.tensor([30000], dtype=torch.int32, device="cuda")
+    at = np.arange(30000 - T, 30000, dtype=np.int64).view(np.uint64)
+    angle = torch.from_numpy(np.multiply.outer(at, table).astype(np.float64) / 2.0 ** 64 * 2.0 * np.pi).cuda()[:, None]
+    dq = x[:T].clone()
+    dk = torch.zeros((1, 1, 30000, d), device="cuda")
+    dk[0, 0, 30000 - T:] = x[T:, 0]
+    outs = [torch.empty((1, T, h, d), device="cuda") for h in (H, 1, 1)]
+    lib().rope_append_bwd(dq[None], dk, dk.clone(), *outs, kv, dev, rp)
+    assert _status() == 0
+    c, s = angle.cos() * scale, -angle.sin() * scale
+    for got, g in ((outs[0][0], dq), (outs[1][0], x[T:, :1])):
+        assert rms(got, turn(g.double(), c, s)) <= rms(turn(g, c.float(), s.float()), turn(g.double(), c, s))
