@@ -40,4 +40,25 @@ INFLLMV2_HD PackedRow packed_row(const int* cu, int B, int r, int rows, int Tq) 
     return PackedRow{lo, r - first, whole ? end - first : 0};
 }
 
+// A row of V elements in memory's chunks of N, chunk k the row's elements k*N - skew and on, `skew` the
+// row's distance from a chunk's boundary.  The first and the last chunk may hold elements of the rows beside
+// it, and the last one may reach past the tensor; then it is not loaded whole (open_end false).
+template <int N>
+struct RowChunks {
+    int skew, V;
+    bool open_end;
+    INFLLMV2_HD int chunks() const { return (skew + V + N - 1) / N; }
+    INFLLMV2_HD int whole() const { return (skew + V) / N; }  // chunks [skew != 0, whole) are uncut
+    INFLLMV2_HD int end() const { return open_end ? chunks() : whole(); }  // chunks [0, end) lie in the tensor
+    INFLLMV2_HD bool cut(int k) const { return k >= whole() || (k == 0 && skew != 0); }
+};
+// Row `row` of a tensor of `rows` rows that starts on a chunk's boundary.
+template <int N>
+INFLLMV2_HD RowChunks<N> row_chunks(unsigned long long row, unsigned long long rows, int V) {
+    const unsigned long long first = row * V;
+    RowChunks<N> c{static_cast<int>(first % N), V, true};
+    c.open_end = first - c.skew + static_cast<unsigned long long>(c.chunks()) * N <= rows * V;
+    return c;
+}
+
 }  // namespace infllmv2

@@ -34,6 +34,7 @@
 // instead of 8 CTAs: 11.7 instead of 12.6.  Rows kept in registers from sweep to sweep spilled and were
 // slower (15.6).
 #include "internal.h"
+#include "places.h"
 #include "tma.cuh"
 
 namespace infllmv2 {
@@ -156,18 +157,15 @@ __device__ __forceinline__ bool stands(float u, u64 Z, float q, u64 w, u64 R) {
 
 // ---- rows
 
-// A row in 16-byte chunks of memory: chunk k holds elements k*N - skew .. of the row, `skew` the row's
-// distance from a 16-byte boundary.  The first and the last chunk may hold elements of the rows beside
-// it; the last one of the tensor's last row (open_end false) is not read past the tensor.
+// A row in 16-byte chunks of memory.
 template <typename T>
-struct RowView {
+struct RowView : RowChunks<16 / sizeof(T)> {
     static constexpr int N = 16 / sizeof(T);
     const T* p;
-    int skew, V;
-    bool open_end;
-    __device__ __forceinline__ int chunks() const { return (skew + V + N - 1) / N; }
-    __device__ __forceinline__ int whole() const { return (skew + V) / N; }  // chunks [skew != 0, whole) are uncut
-    __device__ __forceinline__ int end() const { return open_end ? chunks() : whole(); }  // of those load() reads
+    using RowChunks<N>::skew;
+    using RowChunks<N>::V;
+    using RowChunks<N>::whole;
+    __device__ __forceinline__ RowView(const T* row, const RowChunks<N>& c) : RowChunks<N>(c), p(row) {}
     // Chunk k if `want`, else 0.  One predicated load, so that several in a row are in flight together
     // (a branch around each load would make them wait for one another).
     __device__ __forceinline__ uint4 load(int k, bool want) const {
@@ -181,7 +179,6 @@ struct RowView {
             : "l"(p - skew + static_cast<long long>(k) * N), "r"(want ? 1 : 0));
         return r;
     }
-    __device__ __forceinline__ bool cut(int k) const { return k >= whole() || (k == 0 && skew != 0); }
     // What a cut chunk holds of other rows becomes 0.
     __device__ __forceinline__ void trim(uint4& x, int k) const {
         const int a = k * N - skew;
@@ -200,7 +197,7 @@ struct RowView {
             x.w = pair(x.w, a + 6);
         }
     }
-    // The cut chunk at the end of the tensor, element by element.
+    // The cut chunk that reaches past the tensor, element by element.
     __device__ __noinline__ uint4 tail() const {
         uint32_t w[4] = {0u, 0u, 0u, 0u};
         const int a = whole() * N - skew;
@@ -558,10 +555,10 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
             const Coef cf = sh.c;
             const u64 out = sh.gone;
             const int node = sh.node;
-            const int skew = static_cast<int>(((at + node) * a.V) % N);
-            const bool open_end = at + node + 1 < static_cast<size_t>(a.B) * a.n;
-            const RowView<T> P{target + static_cast<size_t>(node) * a.V, skew, a.V, open_end};
-            const RowView<T> Q{draft + (draft != nullptr ? static_cast<size_t>(node) * a.V : 0), skew, a.V, open_end};
+            const RowChunks<N> cut = row_chunks<N>(at + node, static_cast<size_t>(a.B) * a.n, a.V);
+            const int skew = cut.skew;
+            const RowView<T> P(target + static_cast<size_t>(node) * a.V, cut);
+            const RowView<T> Q(draft + (draft != nullptr ? static_cast<size_t>(node) * a.V : 0), cut);
             const int per_piece = (P.chunks() + pieces - 1) >> (cl_log + kWarpsLog), its = (per_piece + 31) >> 5;
             const int seg = (its + kSegments - 1) / kSegments;
             const int k0 = min(piece * per_piece, P.chunks()), k1 = min(k0 + per_piece, P.chunks());

@@ -194,6 +194,31 @@ def test_verify_at_its_borders(cuda_lib):
     assert lib().sync_status() == 0
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_rows_of_few_tokens_at_the_tensors_end(cuda_lib, dtype):
+    """Vocabularies of 1 to 17: several rows share the last 16 bytes of the tensor, and the path ends at
+    each of them in turn."""
+    torch = torch_mod()
+    t = torch.float32 if dtype == "fp32" else torch.bfloat16
+    for V in range(1, 18):
+        rng = np.random.default_rng(V)
+        n = 9
+        target = torch.from_numpy(_probs(rng, n, V, 0.5)).to(t)
+        draft = torch.from_numpy(_probs(rng, n, V, 0.5)).to(t)
+        tp, dp = target.double().numpy(), draft.double().numpy()
+        parents = [-1] + list(range(n - 1))
+        tokens = rng.integers(0, V, (n, n)).astype(np.int32)
+        u = np.zeros((n, n), dtype=np.float32)  # every draft stands ...
+        u[:, 0] = rng.random(n)
+        for b in range(n - 1):
+            u[b, b + 1] = 1.0                   # ... up to node b
+        rows = lambda x: x.expand(n, n, V).contiguous().cuda()  # noqa: E731
+        out = _run(to_dev(tokens), rows(target), rows(draft), to_dev(u))
+        for b in range(n):
+            _check(out, b, n, *spec_ref.verify(tokens[b].tolist(), parents, tp, dp, u[b], True))
+    assert lib().sync_status() == 0
+
+
 def test_rejected_siblings_past_the_drafts_weight_change_nothing(cuda_lib):
     """Without replacement R stays at nothing once the rejected siblings' q have used it up, however far
     their sum goes past it: duplicates of a drafted token (sums from 2 to 62), and rows above 1."""

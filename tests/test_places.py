@@ -10,6 +10,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 PROGRAM = r"""
 #include <algorithm>
+#include <cstddef>
 #include <vector>
 #include "places.h"
 using namespace infllmv2;
@@ -50,6 +51,29 @@ extern "C" long long packed(int B, int lo, int hi, int most_rows) {
     }
 }
 
+// Every row of a tensor of `rows` rows of V elements, in chunks of N: the number of loads that reach outside
+// the tensor, of elements of the row that no load takes or two take, and of chunks wrongly called uncut.
+template <int N>
+static long long chunks_wrong(int rows, int V) {
+    long long wrong = 0;
+    for (int row = 0; row < rows; ++row) {
+        const RowChunks<N> c = row_chunks<N>(row, rows, V);
+        std::vector<int> taken(V, 0);
+        wrong += c.chunks() - c.end() > 1 || c.end() > c.chunks();
+        for (int k = 0; k < c.chunks(); ++k)
+            for (int e = 0; e < N; ++e) {
+                const long long x = static_cast<long long>(k) * N - c.skew + e, at = static_cast<long long>(row) * V + x;
+                if (e == 0) wrong += at % N != 0;
+                if (k < c.end()) wrong += at < 0 || at >= static_cast<long long>(rows) * V;
+                if (x >= 0 && x < V) ++taken[x];
+                else wrong += !c.cut(k);
+            }
+        for (int x = 0; x < V; ++x) wrong += taken[x] != 1;
+    }
+    return wrong;
+}
+extern "C" long long chunks(int n, int rows, int V) { return n == 4 ? chunks_wrong<4>(rows, V) : chunks_wrong<8>(rows, V); }
+
 extern "C" int packed_len(const int* cu, int B, int r, int rows, int Tq) { return packed_row(cu, B, r, rows, Tq).len; }
 """
 
@@ -63,7 +87,7 @@ def places(tmp_path_factory):
     subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-Wall", "-Werror", "-shared", "-fPIC", "-I", inc,
                     str(src), "-o", str(so)], check=True)
     lib = ctypes.CDLL(str(so))
-    lib.packed.restype = ctypes.c_longlong
+    lib.packed.restype = lib.chunks.restype = ctypes.c_longlong
     return lib
 
 
@@ -77,3 +101,12 @@ def test_packed_offsets_at_the_ends_of_int32(places):
     for cu in ([0, small], [small, big], [small, 5], [0, big], [big, small], [small, small, 5], [0, big, 5]):
         for r in range(4):
             assert places.packed_len((ctypes.c_int * len(cu))(*cu), len(cu) - 1, r, 4, 4) == 0
+
+
+@pytest.mark.parametrize("n", [4, 8])
+def test_chunks_of_rows_lie_in_the_tensor(places, n):
+    """16-byte chunks of fp32 and bf16 rows: rows of few elements, where more than the last one's chunks
+    reach past the tensor, and longer ones."""
+    for V in list(range(1, 40)) + [77, 100, 257, 1001]:
+        for rows in range(1, 24):
+            assert places.chunks(n, rows, V) == 0, (V, rows)
