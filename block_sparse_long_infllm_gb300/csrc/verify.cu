@@ -277,7 +277,7 @@ struct Shared {
     u64 rem;             // what is left of the target in piece `own`
     int node, own, state;
 };
-enum : int { kSweep = 0, kDraw = 1, kBad = 2 };
+enum : int { kSweep = 0, kDraw = 1, kBad = 2, kLost = 3 };  // kLost: a wait ran out
 
 __device__ __forceinline__ u64 warp_sum(u64 x) {
 #pragma unroll
@@ -309,6 +309,18 @@ __device__ __forceinline__ void send16(uint32_t dst, u64 a, u64 b, uint32_t bar)
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(dst), "l"(a),
                  "l"(b), "r"(bar)
                  : "memory");
+}
+// Whether a phase completed within the limit, the same for every lane: a warp that shuffles behind the wait
+// must not part over it.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+}
+// A CTA whose wait ran out in `round`: its peers may still send to it.  Each of them ends (their waits are
+// bounded too, and this CTA sends no more), and it stays until all have, then until what they sent is here.
+__device__ __noinline__ void outstay(uint64_t* bars, int round) {
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+    if (threadIdx.x < 32)
+        for (int r = round; r < round + 2; ++r) (void)warp_wait(&bars[r & 1], (r >> 1) & 1);
 }
 __device__ __forceinline__ int lowest(u64 x) { return __ffsll(static_cast<long long>(x)) - 1; }
 
@@ -581,10 +593,10 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
             if (warp == 0) {
                 int state = kSweep, own = -1;
                 u64 rem = 0ull;
-                if (!mbar_wait(&sh.bar[buf], (round >> 1) & 1)) {
+                if (!warp_wait(&sh.bar[buf], (round >> 1) & 1)) {
                     if (lane == 0) raise_error(a.err, kDevErrTimeout);
-                    state = kBad;
-                    (void)mbar_wait(&sh.bar[buf], (round >> 1) & 1);  // what is still on its way here may land
+                    state = kLost;
+                    own = round;
                 } else {
                     if (lane == 0) mbar_arrive_expect_tx(&sh.bar[buf], pieces * sizeof(Part));  // the round after the next
                     // a lane sums its pieces; a scan over the lanes orders them
@@ -636,7 +648,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
             __syncthreads();
             const int state = sh.state;
             if (state == kSweep) continue;
-            bad = state == kBad;
+            bad = state != kDraw;
             if (!bad && sh.own == piece) {
                 // the segment (lane i sums the piece's i-th), then the token in it
                 u64 rem = sh.rem, tot = 0ull;
@@ -662,7 +674,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
     const u64 path = idle || bad ? 0ull : sh.on;
     const int count = __popcll(path);
     if (rank == 0 && tid < a.n) {
-        if (tid == 0 && (bad || n < 0)) raise_error(a.err, kDevErrIndex);
+        if (tid == 0 && bad && (idle || sh.state != kLost)) raise_error(a.err, kDevErrIndex);
         if (((path >> tid) & 1ull) != 0ull) {
             const int t = __popcll(path & ((1ull << tid) - 1));
             a.path[at + t] = tid;
@@ -675,6 +687,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
         }
     }
     if (drawn >= 0 && lane == 0) a.out_tokens[at + count - 1] = drawn;
+    if (!idle && sh.state == kLost) outstay(sh.bar, sh.own);
 }
 
 // The row of each of B sequences goes to the largest cluster whose CTAs are all resident at once and

@@ -507,7 +507,8 @@ int infllmv2_rope_drafts(const void* q, int64_t ld_q, const void* k_new, int64_t
  * range, a target row that had to be summed -- the last node's, or one with
  * children left after a rejection -- with a sum above 2, or the last node's with
  * a sum of 0) set the error word; that sequence's outputs are those of an idle
- * one: n_path 0, -1 elsewhere, kv_len unchanged.
+ * one: n_path 0, -1 elsewhere, kv_len unchanged.  (After a wait that ran out,
+ * INFLLMV2_ERR_DEVICE_TIMEOUT, a sequence's outputs are undefined.)
  * Needs no workspace.  n_draft <= 64, V <= 2^24.
  */
 int infllmv2_verify(const int32_t* tokens, const uint64_t* tree_mask, const int32_t* n_nodes, const void* target,

@@ -279,3 +279,15 @@ def test_binding_takes_parameters_as_dicts_and_structures(built_lib):
         L.rope(**dict(a["rope"], rope=L.Params.make(P)))
     with pytest.raises(ValueError, match="freqs"):
         L.rope(**dict(a["rope"], rope=dict(rotary_dim=32)))
+
+
+def test_verification_waits_are_decided_by_whole_warps():
+    """A lane that gives up a bounded wait alone parts its warp, and the other lanes' full-mask shuffles
+    behind the wait have no defined end.  (A wait that runs out cannot be provoked by a valid call.)"""
+    import os
+    import re
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "block_sparse_long_infllm_gb300",
+                        "csrc", "verify.cu")
+    text = re.sub(r"//[^\n]*", "", open(path).read())
+    waits = [text[max(m.start() - 40, 0):m.start()] for m in re.finditer(r"\bmbar_(try_|test_)?wait\(", text)]
+    assert waits and all(w.rstrip().endswith("__all_sync(0xffffffffu,") for w in waits)
