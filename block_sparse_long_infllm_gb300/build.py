@@ -3,12 +3,13 @@
 Each translation unit compiles in parallel to `_build/`, then nvcc links the
 shared library next to this file.  The CUDA runtime is linked as a shared
 library so the process shares one runtime (and one set of stream handles)
-with PyTorch.  `_binding.so` (csrc/binding.cpp, the host compiler) is linked to
-that library and to PyTorch's.
+with PyTorch.  That needs nvcc alone.  Where PyTorch is installed, `_binding.so`
+(csrc/binding.cpp, the host compiler) is then linked to that library and to PyTorch's.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -39,10 +40,15 @@ def _inputs() -> list[str]:
     return files
 
 
+def _with_binding() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
+    outputs = [LIB_PATH] + ([BINDING_PATH] if _with_binding() else [])
+    if not all(os.path.exists(f) for f in outputs):
         return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
+    t = min(os.path.getmtime(f) for f in outputs)
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
@@ -98,9 +104,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = ex.submit(_compile_binding) if _with_binding() else None
         results = list(ex.map(compile_one, SOURCES))
-        binding_obj = binding.result()
     if verbose or ptxas_info:
         for _, log in results:
             if log:
@@ -111,7 +116,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    _link_binding(binding_obj)
+    if binding is not None:  # a fault of the binding's leaves the library in place
+        _link_binding(binding.result())
     return LIB_PATH
 
 
