@@ -253,6 +253,34 @@ def test_verify_reads_bad_numbers_as_documented(cuda_lib):
     assert lib().sync_status() == 0
 
 
+@pytest.mark.parametrize("replace", [True, False])
+def test_draft_rows_of_bad_numbers_are_read_as_documented(cuda_lib, replace):
+    """NaN, infinite, negative and large values in the draft rows of visited nodes (and NaN and negative ones in
+    the target's), against the exact rationals, which read them as the header says."""
+    nan, inf = float("nan"), float("inf")
+    bad = [nan, inf, -inf, -0.5, 7.0, 1e38, -0.0, 1e-40]
+    # by hand: q(1) = inf is read as 1 and p - q leaves token 0; q(1) = NaN or below 0 is 0 and token 1 stands
+    half = [0.5, 0.5, 0.0, 0.0]
+    for q, want in ((inf, ([0], [0])), (7.0, ([0], [0])), (nan, ([0, 1], [1, 0])), (-1.0, ([0, 1], [1, 0]))):
+        assert _one([half] * 2, [[0.25, q, 0, 0]] * 2, [0, 1], [0.0, 0.75], [-1, 0], replace=replace) == want
+    rng = np.random.default_rng(17)
+    lengths = set()
+    for _ in range(60):
+        n, V = 8, 6
+        target, draft = _probs(rng, n, V, 1.0), _probs(rng, n, V, 1.0)
+        for row in range(n):
+            draft[row, rng.choice(V, 2, replace=False)] = rng.choice(bad, 2)
+            target[row, rng.integers(V)] = rng.choice([nan, -inf, -1.0, 0.25])
+        parents = random_tree(rng, n, 4)
+        tokens = rng.integers(0, V, n).tolist()
+        u = rng.random(n).astype(np.float32).tolist()
+        want = spec_ref.verify(tokens, parents, target, draft, u, replace)
+        assert _one(target, draft, tokens, u, parents, replace=replace) == want
+        lengths.add(len(want[0]))
+    assert len(lengths) > 1
+    assert lib().sync_status() == 0
+
+
 def test_verify_reports_bad_sequences_and_keeps_the_others(cuda_lib):
     torch = torch_mod()
     L = lib()
@@ -425,6 +453,29 @@ def test_commit_skips_bad_sequences_and_reports(cuda_lib):
     assert float(k[0, 0, 6:10].sum()) == 4 * d and float(k[0].sum()) == 4 * d
     assert float(kern[0, 0, 3, 0]) == 1.0
     assert L.sync_status() == 0
+
+
+def test_commit_without_kernel_cache(cuda_lib):
+    """Caches that hold no kernel yet need no kernel cache; a sequence whose path would complete one is
+    skipped and reported."""
+    torch = torch_mod()
+    L = lib()
+    B, n, d, room = 3, 4, 128, 64
+    p = dict(block_size=64, kernel_size=32, kernel_stride=16, topk=4, n_init_blocks=1, n_local_blocks=2, dense_len=0)
+    draft = torch.arange(1, n + 1, device="cuda", dtype=torch.float32).to(torch.bfloat16)[:, None].expand(B, 2, n, d).contiguous()
+    k, v = (torch.zeros((B, 2, room, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    path = torch.tensor([[0, 2, 3, -1]] * B, dtype=torch.int32, device="cuda")
+    m = torch.full((B,), 3, dtype=torch.int32, device="cuda")
+    L.commit(draft, draft.clone(), path, m, k, v, None, torch.tensor([3, 31, 20], dtype=torch.int32, device="cuda"), p)
+    assert L.sync_status() == 0
+    for b, end in enumerate((3, 31, 20)):
+        for cache in (k, v):
+            assert cache[b, :, end - 3:end, 0].tolist() == [[1.0, 3.0, 4.0]] * 2
+            assert float(cache[b].sum()) == 8.0 * 2 * d
+    k.zero_(), v.zero_()
+    L.commit(draft, draft.clone(), path, m, k, v, None, torch.tensor([31, 32, 50], dtype=torch.int32, device="cuda"), p)
+    assert L.sync_status() == L.ERR_DEVICE_INDEX
+    assert float(k[0].sum()) == 8.0 * 2 * d and float(k[1:].sum()) == float(v[1:].sum()) == 0.0
 
 
 # ---- the loop as a serving program runs it

@@ -2,7 +2,8 @@
 launch, and the binding refuses tensors of other types and shapes -- all without a GPU.  The table
 of frequencies is checked against 50-digit arithmetic."""
 import ctypes
-from decimal import Decimal, getcontext
+import math
+from decimal import ROUND_CEILING, ROUND_FLOOR, Decimal, getcontext
 
 import pytest
 
@@ -171,6 +172,34 @@ def test_freqs_scalings(built_lib):
     lng, m = L.rope_freqs(rot, base, "divisors", factor=s, orig_len=L0, divisors=div)
     assert torch.allclose(lng.double() * div.double(), plain, rtol=2 ** -40)
     assert abs(m - 1.1180339887498949) < 1e-6  # sqrt(1 + ln 8 / ln 4096) = sqrt(1.25)
+
+
+@pytest.mark.parametrize("rot,base,s,L0,fast,slow", [
+    (64, 10000.0, 8.0, 4096, 32.0, 1.0), (128, 10000.0, 4.0, 32768, 32.0, 1.0), (128, 500000.0, 16.0, 8192, 32.0, 1.0),
+    (96, 1e6, 2.0, 2048, 16.0, 2.0), (32, 10000.0, 40.0, 4096, 64.0, 0.5), (64, 10000.0, 8.0, 128, 32.0, 1.0)])
+def test_freqs_yarn_between_its_ends(built_lib, rot, base, s, L0, fast, slow):
+    """Every pair against the formula in 50 digits: the ramp over i runs from the pair (rounded down) that turns
+    beta_fast times within orig_len tokens to the one (rounded up) that turns beta_slow times."""
+    _pi()
+    D = Decimal
+    two_pi = 2 * _pi()
+
+    def pair(turns):
+        return D(rot) * (D(L0) / (D(turns) * two_pi)).ln() / (2 * D(base).ln())
+
+    low = max(int(pair(fast).to_integral_value(ROUND_FLOOR)), 0)
+    high = min(int(pair(slow).to_integral_value(ROUND_CEILING)), rot - 1)
+    freqs, scale = L.rope_freqs(rot, base, "yarn", factor=s, orig_len=L0, beta_fast=fast, beta_slow=slow)
+    assert abs(scale - (0.1 * math.log(s) + 1)) <= 2 ** -23
+    between = 0
+    for i, f in enumerate(freqs.tolist()):
+        theta = (D(base).ln() * D(-2 * i) / D(rot)).exp()
+        ramp = min(max(D(i - low) / D(high - low), D(0)), D(1))
+        turns = (theta / D(s) * ramp + theta * (1 - ramp)) / two_pi
+        between += 0 < ramp < 1
+        # fp64: pow within 1 ulp, then a handful of operations, and the cut to 2^-64
+        assert abs(D(f % (1 << 64)) / D(1 << 64) - turns) <= turns * D(2) ** -48 + D(2) ** -63, i
+    assert between >= 3
 
 
 @pytest.mark.parametrize("kw", [
