@@ -15,7 +15,7 @@ namespace infllmv2 {
 // units of 2^-33 of a turn (its rounding: 2 pi 2^-34 < 2^-31), and the angle a + b = 2 pi 2^-33 n two fp32
 // numbers.  Taylor's series in z = a^2 up to a^9 and a^10: the first term left out is below 2^-28 of sin
 // and 2^-33.  Both end in one product and sum with `scale`: with cos - 1 rounded before it (it is at most
-// 0.293: 2^-26), off by half a unit in the last place and 2^-25.9 of the scale.
+// 0.293: 2^-26), off by half a unit in the last place and 2^-25.4 of the scale.
 INFLLMV2_HD void cos_sin_of_turn(unsigned long long turn, float scale, float* c_out, float* s_out) {
     const unsigned quarter = static_cast<unsigned>((turn + (1ull << 61)) >> 62);
     const long long rest = static_cast<long long>(turn - (static_cast<unsigned long long>(quarter) << 62));

@@ -15,7 +15,8 @@
 // become integers by a shift, differences and sums of integers are exact and independent of their
 // order, so every cluster size samples the same token (fp32 sums would move the border between two
 // tokens by more than a rare token's probability, and this GPU's fp64 rate is a few operations per
-// clock and SM).
+// clock and SM).  After one rejection c is 1 and w exact; from the second on c is a sum of quotients, each
+// rounded at 2^-60 of itself, and c q is cut to whole units.
 //
 // What bounds it is memory: the last node's target row (and draft row, once a child was rejected).
 // One thread-block cluster per sequence; a row is cut into one contiguous piece per warp.  In each
@@ -27,10 +28,10 @@
 // stand at their first trial lead by comparing masks.
 //
 // Measured on a GB300 (programmatic launches back to back): one tree of 16 drafts over 32001 tokens,
-// two to three sweeps, 10.7 us, and 6.7 us where one sweep does; 64 chains of 8 over 131072 tokens 21.5
+// two to three sweeps, 10.7 us, and 6.7 us where one sweep does; 64 chains of 8 over 131072 tokens 21.7
 // us, of which about 12 move the 67 MB (10.0 us at the copy rate), 3.5 pass before the last node is known
 // (tokens, then their probabilities: two loads that miss every cache) and 2.5 after the sums.  Cluster
-// sizes for them: 8 21.5, 4 27, 16 40; CTAs per SM: 4 (64 registers) 21.5, 3 27.6, 2 25.6.  For one tree 16
+// CTAs per SM: 4 (64 registers) 21.5, 3 27.6, 2 25.6; cluster sizes are with launch() below.  For one tree 16
 // instead of 8 CTAs: 11.7 instead of 12.6.  Rows kept in registers from sweep to sweep spilled and were
 // slower (15.6).
 #include "internal.h"
@@ -690,9 +691,17 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident) verify_kernel(Verif
     if (!idle && sh.state == kLost) outstay(sh.bar, sh.own);
 }
 
-// The row of each of B sequences goes to the largest cluster whose CTAs are all resident at once and
-// whose warps each have at least 32 chunks; to more than 8 CTAs only for up to 16 sequences (8 chains of 8
-// over 131072 tokens: 16 CTAs 10.0 us, 8 11.6; 16 chains 12.1 and 13.6; 64 chains 40 and 21.5).
+// The row of each of B sequences goes to the largest cluster (a power of two) whose CTAs are all resident at
+// once and whose warps each have at least 32 chunks; to more than 8 CTAs only for up to 16 sequences.  us
+// for B chains of 8 over 131072 fp32 tokens by CTAs per cluster, the rule's choice in brackets:
+//     B      8     16     17     32     38     48     64     77    100    152    200    304    608
+//    16 [10.2] [12.6]  14.5   18.0   20.3   23.2   27.9   32.2
+//     8  11.7   13.4  [13.9] [15.0] [21.0] [21.2] [21.8]  26.5   32.8   42.1
+//     4         17.9   18.1   18.5   22.0   22.8   23.5  [34.7] [34.9] [40.4]  50.8   66.3
+//     2                       29.5   30.6   30.8   30.9   35.6   38.6   40.3  [61.8] [63.0] 112.7
+//     1                                            54.2   55.0   55.4   56.2   70.2   72.6 [118.0]
+// Up to 64 sequences it is within 4 % of the best power of two.  Just past the sizes that fit at once (64, 152, 304)
+// twice as many CTAs in two waves would still be faster, by up to a quarter.
 template <typename T>
 cudaError_t launch(const VerifyArgs& a) {
     int cl_log = a.B <= 16 ? 4 : 3;

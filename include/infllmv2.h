@@ -366,7 +366,8 @@ int infllmv2_decode_step(const void* q, const void* k_new, const void* v_new, vo
  * (i < rotary_dim / 2) is elements i and rotary_dim/2 + i, or, interleaved, 2i
  * and 2i + 1.  In the row at position x it turns by x * theta_i:
  *   y_a = attn_scale (a cos - b sin),  y_b = attn_scale (a sin + b cos)
- * in fp32, rounded once; elements from rotary_dim on are copied bit for bit.
+ * in fp32 (cos and sin, attn_scale in them, to 2^-23 of attn_scale), rounded once;
+ * elements from rotary_dim on are copied bit for bit.
  */
 typedef struct infllmv2_rope_params {
     int32_t rotary_dim;   /* leading elements of a head that turn: even, 2 .. d      */
@@ -394,8 +395,9 @@ enum { INFLLMV2_BF16 = 0, INFLLMV2_FP32 = 1 };
 /*
  * Host helper: the table of frequencies that the entry points below read from
  * device memory.  freqs_host[i] = floor(frac(theta_i / 2 pi) * 2^64), the turns
- * per position in units of 2^-64: position times it, modulo 2^64, is the
- * fraction of a turn for every int32 position, so far positions lose nothing.
+ * per position in units of 2^-64, computed in fp64: position times it, modulo
+ * 2^64, is the fraction of a turn, with no rounding of its own for any int32
+ * position.
  * Writes rotary_dim / 2 entries and, when attn_scale is not NULL, the scaling's
  * factor.  base > 1; factor > 0 is read by every scaling but PLAIN; orig_len > 1
  * by YARN and DIVISORS; beta_fast > beta_slow > 0 by YARN; divisors
@@ -489,8 +491,10 @@ int infllmv2_rope_drafts(const void* q, int64_t ld_q, const void* k_new, int64_t
  *   draft == NULL: x stands iff u[x] Z < w(x); otherwise Z loses w(x), w(x) = 0.
  * The first child that stands is the next node; where none does, the last token
  * is the first one whose running sum of w passes u[0] * (sum of w), or of p when
- * w has nothing left.  Sums are exact, in units of 2^-62 (what of a probability
- * lies below that is dropped); comparisons are exact.
+ * w has nothing left.  Weights are held in units of 2^-62 (what of a probability
+ * lies below that is dropped); their sums and the comparisons are exact.  So is w
+ * after one rejection at a node; from the second on the factor of q in w, a sum of
+ * the quotients Z/R, is rounded at 2^-60 of itself, and its product with q at 2^-62.
  *   tokens    [B, n_draft] int32; a root's is not read
  *   tree_mask [B, n_draft], NULL: a chain (node i's parent is i - 1)
  *   n_nodes   [B] int32 in [0, n_draft], nodes in use (0: the sequence is idle);
