@@ -143,7 +143,8 @@ cudaError_t launch_append(const void* k_new, const void* v_new, void* k_cache, v
 // loads (the path, then rows) and the pooling's chain of shuffles, 2.3 us for one sequence of 16 drafts;
 // for many sequences also how many CTAs are resident, so kernels of at most 32 tokens (the pages' size)
 // have their own instance with two rows per lane (48 registers instead of 87): 32 sequences x 8 heads
-// of 64 drafts 8.6 us, with half of the issue slots empty.  Pooling two (four) kernels per CTA, with fewer CTAs, took 11.1 (14.2) us.
+// of 64 drafts 8.6 us, with half of the issue slots empty.  Pooling two (four) kernels per CTA, with fewer
+// CTAs, took 11.1 (14.2) us.
 template <int D, int kRows>
 __global__ void __launch_bounds__(2 * D, kRows == 2 ? 640 / D : 1) commit_kernel(
     const __nv_bfloat16* __restrict__ dk, const __nv_bfloat16* __restrict__ dv, const int* __restrict__ path,
