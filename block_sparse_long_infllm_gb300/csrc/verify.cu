@@ -16,7 +16,9 @@
 // order, so every cluster size samples the same token (fp32 sums would move the border between two
 // tokens by more than a rare token's probability, and this GPU's fp64 rate is a few operations per
 // clock and SM).  After one rejection c is 1 and w exact; from the second on c is a sum of quotients, each
-// rounded at 2^-60 of itself, and c q is cut to whole units.
+// rounded up by less than 2^-58 of itself, and c q is cut to whole units: where the rejections leave the
+// target nothing (one token with all of w, and with all that is left of the drafts), nothing is left here
+// too, since c' q = (c + Z/R) q is at least what c q was cut to and Z = w, together p.
 //
 // What bounds it is memory: the last node's target row (and draft row, once a child was rejected).
 // One thread-block cluster per sequence; a row is cut into one contiguous piece per warp.  In each
@@ -30,10 +32,9 @@
 // Measured on a GB300 (programmatic launches back to back): one tree of 16 drafts over 32001 tokens,
 // two to three sweeps, 10.7 us, and 6.7 us where one sweep does; 64 chains of 8 over 131072 tokens 21.7
 // us, of which about 12 move the 67 MB (10.0 us at the copy rate), 3.5 pass before the last node is known
-// (tokens, then their probabilities: two loads that miss every cache) and 2.5 after the sums.  Cluster
-// CTAs per SM: 4 (64 registers) 21.5, 3 27.6, 2 25.6; cluster sizes are with launch() below.  For one tree 16
-// instead of 8 CTAs: 11.7 instead of 12.6.  Rows kept in registers from sweep to sweep spilled and were
-// slower (15.6).
+// (tokens, then their probabilities: two loads that miss every cache) and 2.5 after the sums.  CTAs per SM:
+// 4 (64 registers) 21.5, 3 27.6, 2 25.6; cluster sizes are with launch() below.  For one tree 16 instead of
+// 8 CTAs: 11.7 instead of 12.6.  Rows kept in registers from sweep to sweep spilled and were slower (15.6).
 #include "internal.h"
 #include "places.h"
 #include "tma.cuh"
@@ -89,31 +90,40 @@ __device__ __forceinline__ Num num(u64 x) {
     const int z = __clzll(static_cast<long long>(x));
     return Num{x << z, 1 - z};
 }
+// a + b, rounded up.
 __device__ __forceinline__ Num add(Num a, Num b) {
     if (a.e < b.e) {
         const Num t = a;
         a = b;
         b = t;
     }
-    Num r{a.m + shr(b.m, a.e - b.e), a.e};
+    const int d = a.e - b.e;
+    const u64 s = shr(b.m, d);
+    Num r{a.m + s + (d < 64 && (s << d) == b.m ? 0ull : 1ull), a.e};
     if (r.m < a.m) {
-        r.m = (r.m >> 1) | (1ull << 63);
+        r.m = (r.m >> 1) + (r.m & 1ull) + (1ull << 63);
         ++r.e;
     }
     return r;
 }
-// a / b: two Newton steps from an fp32 reciprocal, y -> y + y (1 - b y), y 2^-62 the reciprocal of b's
-// mantissa in [1, 2): 2^-23, 2^-46, then the arithmetic's 2^-60.
+// a / b, rounded up by less than 2^-58 of it: two Newton steps from an fp32 reciprocal, y -> y + y (1 - b y),
+// y 2^-62 the reciprocal of b's mantissa in [1, 2): 2^-23, 2^-46, then less than 2^-59 below the quotient (a
+// unit of y, at least 2^61, and one of q, at least 2^60), which the 32 of at most 2^64 make up for.
 __device__ __forceinline__ Num divide(Num a, Num b) {
     u64 y = static_cast<u64>(__fdiv_rn(0x1p62f, __ull2float_rn(b.m) * 0x1p-63f));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const long long err = static_cast<long long>((1ull << 61) - __umul64hi(b.m, y));  // (1 - b y) 2^61
-        y += static_cast<u64>(__mul64hi(static_cast<long long>(y), err) * 8);
+        const long long err = static_cast<long long>((1ull << 61) - __umul64hi(b.m, y));  // (1 - b y) 2^61, below 2^40
+        y += static_cast<u64>(__mul64hi(static_cast<long long>(y), err * 8));
     }
     const u64 q = __umul64hi(a.m, y);  // quotient of the mantissas in (1/2, 2), times 2^61
     const int z = __clzll(static_cast<long long>(q));
-    return Num{q << z, a.e - b.e + 2 - z};
+    Num r{(q << z) + 32ull, a.e - b.e + 2 - z};
+    if (r.m < 32ull) {
+        r.m = (1ull << 63) + 16ull;
+        ++r.e;
+    }
+    return r;
 }
 
 // c, the factor of the draft's row in w.

@@ -494,7 +494,8 @@ int infllmv2_rope_drafts(const void* q, int64_t ld_q, const void* k_new, int64_t
  * w has nothing left.  Weights are held in units of 2^-62 (what of a probability
  * lies below that is dropped); their sums and the comparisons are exact.  So is w
  * after one rejection at a node; from the second on the factor of q in w, a sum of
- * the quotients Z/R, is rounded at 2^-60 of itself, and its product with q at 2^-62.
+ * the quotients Z/R, is rounded up by less than 2^-57 of itself, and its product
+ * with q down to whole units.
  *   tokens    [B, n_draft] int32; a root's is not read
  *   tree_mask [B, n_draft], NULL: a chain (node i's parent is i - 1)
  *   n_nodes   [B] int32 in [0, n_draft], nodes in use (0: the sequence is idle);

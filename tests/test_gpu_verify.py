@@ -194,6 +194,37 @@ def test_verify_at_its_borders(cuda_lib):
     assert lib().sync_status() == 0
 
 
+def test_weights_that_cancel_after_a_quotient_leave_nothing(cuda_lib):
+    """Without replacement, with twins among the siblings: one token has all of w, and the drafts have nothing
+    but it left, so the next rejection takes all of it, to the last unit although Z/R is no binary
+    fraction.  The last token then comes from p."""
+    # Z = 0.2578125, R = q(1) = 0.47265625
+    p, q = [0.267578125, 0.73046875], [0.52734375, 0.47265625]
+    tokens, parents, u = [0] * 5, [-1, 0, 0, 0, 0], [0.0341401, 0.9172202, 0.9963093, 0.9445311, 0.9634557]
+    want = spec_ref.verify(tokens, parents, [p] * 5, [q] * 5, u, False)
+    assert want == ([0], [0])
+    assert _one([p] * 5, [q] * 5, tokens, u, parents, replace=False) == want
+    # rows of 2 to 4 tokens in 512ths; siblings take the tokens in turn, then again from the first
+    rng = np.random.default_rng(29)
+    for V in (2, 3, 4):
+        B, n = 400, 2 * V + 1
+        cuts = np.sort(rng.integers(0, 513, (2, B, V - 1)), -1)
+        rows = np.diff(np.concatenate([np.zeros((2, B, 1)), cuts, np.full((2, B, 1), 512)], -1), axis=-1) / 512
+        target, draft = (np.repeat(r[:, None], n, 1).astype(np.float32) for r in rows)
+        tokens = np.zeros((B, n), dtype=np.int32)
+        for b in range(B):
+            order = rng.permutation(V)
+            tokens[b, 1:] = np.concatenate([order[:V - 1], order[:V - 1], order[:2]])
+        u = (1 - rng.random((B, n)) * 1e-3).astype(np.float32)
+        u[:, 0] = rng.random(B)
+        masks = to_dev(np.array([masks_of([-1] + [0] * (n - 1))] * B, dtype=np.uint64))
+        out = _run(to_dev(tokens), to_dev(target), to_dev(draft), to_dev(u), tree_mask=masks, replace=False)
+        for b in range(B):
+            _check(out, b, n, *spec_ref.verify(tokens[b].tolist(), [-1] + [0] * (n - 1), target[b].astype(np.float64),
+                                               draft[b].astype(np.float64), u[b], False))
+    assert lib().sync_status() == 0
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_rows_of_few_tokens_at_the_tensors_end(cuda_lib, dtype):
     """Vocabularies of 1 to 17: several rows share the last 16 bytes of the tensor, and the path ends at
