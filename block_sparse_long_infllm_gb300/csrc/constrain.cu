@@ -705,9 +705,11 @@ cudaError_t launch_kind(const ConstrainArgs& a, int parts, int piece, int cluste
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
-    const int smem = kStaged ? (piece + 4) * kWarps * static_cast<int>(sizeof(float)) : 0;
-    if (smem > 24 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const auto bytes = [](int n) { return (n + 4) * kWarps * static_cast<int>(sizeof(float)); };
+    const int smem = kStaged ? bytes(piece) : 0;
+    if (kStaged) {
+        // (the limit belongs to the function and all host threads share it: each call sets the same one, the largest)
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(kMostPiece));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
