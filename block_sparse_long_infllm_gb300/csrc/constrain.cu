@@ -407,12 +407,13 @@ __global__ void __launch_bounds__(kThreads, kProbs ? kResident : kResidentLogits
         const unsigned short* const history = a.history != nullptr ? a.history + b * a.ld_history + begin : nullptr;
         const float shrink = 1.f / c.repetition;
 
-        // the drafts on the way: each warp looks for those in its piece and makes their logits
+        // the drafts on the way (a root has none, but its mask is checked like the others'): each warp looks for those
+        // in its piece and makes their logits
         unsigned mine = 0u;
         int n_fixes = 0;
+        const u64 way = a.tree_mask != nullptr ? a.tree_mask[row] : ~0ull >> (63 - node);
+        if (a.n < 64) bad = bad || (way >> a.n) != 0ull;
         if (a.tokens != nullptr && node > 0) {
-            const u64 way = a.tree_mask != nullptr ? a.tree_mask[row] : ~0ull >> (63 - node);
-            if (a.n < 64) bad = bad || (way >> a.n) != 0ull;
             __syncwarp();  // the last row's were read
 #pragma unroll 1
             for (int k = lane; k < (a.n + 31) / 32 * 32; k += 32) {

@@ -568,7 +568,8 @@ int infllmv2_norm_rope_append_bwd(const float* dq, const float* dk, const float*
  *                 pointer, ld and type) and overlaps nothing else
  *   tokens        [B, n_draft] int32, the drafts (a root's is not read); NULL: no
  *                 drafts are counted
- *   tree_mask     [B, n_draft] as for infllmv2_decode; NULL: a chain
+ *   tree_mask     [B, n_draft] as for infllmv2_decode, given with tokens alone;
+ *                 NULL: a chain
  *   n_nodes       [B] int32 in [0, n_draft], nodes in use; rows behind them are
  *                 left as they are; NULL: n_draft everywhere
  *   history       [B] rows of ld_history 16-bit counts of the V tokens: bit 15 in
@@ -580,8 +581,8 @@ int infllmv2_norm_rope_append_bwd(const float* dq, const float* dk, const float*
  *   controls      [B, 4] fp32: repetition (> 0), frequency, presence, temperature
  *                 (>= 0), all finite; NULL: 1, 0, 0, 1
  * Device errors (controls out of range, n_nodes out of range, a token of a draft on
- * a row's way outside [0, V), bits of a mask from n_draft on) set the error word;
- * those rows become zeros (probs == 0: -inf).
+ * a row's way outside [0, V), bits of a row's mask from n_draft on, the root's too)
+ * set the error word; those rows become zeros (probs == 0: -inf).
  * V <= 2^24; at most 2^18 rows.
  */
 int infllmv2_constrain(const void* logits, int64_t ld, const int32_t* tokens, const uint64_t* tree_mask,
