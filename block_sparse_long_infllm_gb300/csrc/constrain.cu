@@ -773,6 +773,7 @@ constexpr int kHistSlice = 16384;  // tokens of the vocabulary that a CTA counts
 constexpr int kMarkSlice = 32768;  // the same of a prompt's tokens
 constexpr int kHistUnroll = 2;     // loads of four tokens under way
 constexpr int kFewTokens = 128;    // generated tokens of a sequence, on average, that one CTA counts alone
+constexpr int kFewLongest = 1024;  // the same of packed ones, of which one may have nearly all
 constexpr int kFewMarks = 32768;   // tokens of prompts, of all sequences, that are marked one by one
 
 // How a 16-bit count takes n more of its token.
@@ -795,16 +796,44 @@ __device__ __forceinline__ Text text_of(const CountArgs& a, int b) {
     return Text{lo, bad ? -1 : hi - lo};
 }
 
+// The sequence of the which-th list (from 0) of more than kFewLongest tokens, or -1, found by the whole CTA.
+__device__ int long_list(const CountArgs& a, int which) {
+    __shared__ int in_warp[kHistThreads / 32], found;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    for (int first = 0; first < a.B; first += kHistThreads) {
+        const bool is = first + tid < a.B && text_of(a, first + tid).n > kFewLongest;
+        const unsigned ones = __ballot_sync(kAll, is);
+        if (lane == 0) in_warp[warp] = __popc(ones);
+        const int here = __syncthreads_count(is);
+        if (which < here) {
+            int rank = __popc(ones & ((1u << lane) - 1u));
+            for (int w = 0; w < warp; ++w) rank += in_warp[w];
+            if (is && rank == which) found = first + tid;
+            __syncthreads();
+            return found;
+        }
+        which -= here;
+        __syncthreads();
+    }
+    return -1;
+}
+
 // One CTA counts a slice of the vocabulary over all of a sequence's tokens, in shared memory, and then owns the
 // slice of the row: no atomics on global memory, however often a token comes.  A prompt's tokens are marked in
-// bytes (of 0x80, the sign of a 16-bit word), so a slice can be longer.
-template <bool kPrompt>
+// bytes (of 0x80, the sign of a 16-bit word), so a slice can be longer.  kLong: of long lists alone.
+template <bool kPrompt, bool kLong>
 __global__ void __launch_bounds__(kHistThreads) count_slice_kernel(CountArgs a, bool vectors) {
     using Cell = std::conditional_t<kPrompt, unsigned char, int>;
     constexpr int kSlice = kPrompt ? kMarkSlice : kHistSlice;
     extern __shared__ int4 cells4[];
     Cell* const cells = reinterpret_cast<Cell*>(cells4);
-    const int b = blockIdx.y, tid = threadIdx.x;
+    const int tid = threadIdx.x;
+    int b = blockIdx.y;
+    if constexpr (kLong) {
+        pdl_wait();
+        b = long_list(a, b);
+        if (b < 0) return;
+    }
     const int begin = blockIdx.x * kSlice, width = min(kSlice, a.V - begin);
     for (int i = tid; i < kSlice * static_cast<int>(sizeof(Cell)) / 16; i += kHistThreads) cells4[i] = make_int4(0, 0, 0, 0);
     pdl_wait();
@@ -892,7 +921,8 @@ __global__ void __launch_bounds__(kHistThreads) count_slice_kernel(CountArgs a, 
 }
 
 // Few generated tokens: one CTA per sequence.  The first of each kFewThreads tokens' equals adds all of them, so
-// nothing is added to twice at once.
+// nothing is added to twice at once.  Packed lists of more than kFewLongest are left to the other kernel: 4 us for each
+// kFewThreads tokens, one list of 8192 would take 128 (5.7 there; the other launch costs the rest of such calls 2.1).
 __global__ void __launch_bounds__(kFewThreads) count_few_kernel(CountArgs a) {
     __shared__ alignas(16) int near[kFewThreads];
     const int b = blockIdx.x, tid = threadIdx.x;
@@ -901,8 +931,9 @@ __global__ void __launch_bounds__(kFewThreads) count_few_kernel(CountArgs a) {
     const Text text = text_of(a, b);
     bool bad = text.n < 0;
     unsigned short* const row = a.history + b * a.ld_history;
-    for (int at = 0; at < text.n; at += kFewThreads) {
-        const int n = min(kFewThreads, text.n - at);
+    const int tokens = a.cu != nullptr && text.n > kFewLongest ? 0 : text.n;
+    for (int at = 0; at < tokens; at += kFewThreads) {
+        const int n = min(kFewThreads, tokens - at);
         int t = -1;
         if (tid < n) {
             t = a.tokens[text.first + at + tid];
@@ -970,17 +1001,26 @@ cudaError_t launch_constrain(const ConstrainArgs& a) {
     return a.out_bf16 ? launch<float, bf16>(a) : launch<float, float>(a);
 }
 
+template <bool kPrompt, bool kLong>
+static cudaError_t launch_slices(const CountArgs& a, long long lists) {
+    constexpr int slice = kPrompt ? kMarkSlice : kHistSlice;
+    constexpr int smem = kPrompt ? kMarkSlice : kHistSlice * static_cast<int>(sizeof(int));
+    const auto kern = count_slice_kernel<kPrompt, kLong>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kern, dim3((a.V + slice - 1) / slice, static_cast<unsigned>(lists)), dim3(kHistThreads), smem, a.stream,
+                         true, a, a.ld_history % 8 == 0);
+}
+
 cudaError_t launch_count(const CountArgs& a) {
-    if (a.reset || a.total > (a.prompt ? kFewMarks : static_cast<long long>(a.B) * kFewTokens)) {
-        const auto kern = a.prompt ? count_slice_kernel<true> : count_slice_kernel<false>;
-        const int slice = a.prompt ? kMarkSlice : kHistSlice;
-        const int smem = a.prompt ? kMarkSlice : kHistSlice * static_cast<int>(sizeof(int));
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        return launch_kernel(kern, dim3((a.V + slice - 1) / slice, a.B), dim3(kHistThreads), smem, a.stream, true, a,
-                             a.ld_history % 8 == 0);
+    if (a.reset || a.total > (a.prompt ? kFewMarks : static_cast<long long>(a.B) * kFewTokens))
+        return a.prompt ? launch_slices<true, false>(a, a.B) : launch_slices<false, false>(a, a.B);
+    if (!a.prompt) {
+        const cudaError_t e = launch_kernel(count_few_kernel, dim3(a.B), dim3(kFewThreads), 0, a.stream, true, a);
+        // (offsets in order leave room for no more long lists)
+        const long long lists = a.cu != nullptr ? a.total / (kFewLongest + 1) : 0;
+        return e != cudaSuccess || lists == 0 ? e : launch_slices<false, true>(a, lists);
     }
-    if (!a.prompt) return launch_kernel(count_few_kernel, dim3(a.B), dim3(kFewThreads), 0, a.stream, true, a);
     return launch_kernel(count_mark_kernel, dim3(static_cast<unsigned>((a.total + kFewThreads - 1) / kFewThreads)),
                          dim3(kFewThreads), 0, a.stream, true, a);
 }
