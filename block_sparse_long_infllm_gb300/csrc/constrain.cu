@@ -365,7 +365,10 @@ __global__ void __launch_bounds__(kThreads, kProbs ? kResident : kResidentLogits
         if (bytes != 0u) bulk_load(stage, src, bytes, &full[warp]);
     };
     if (kStaged && row < to) fetch();
-    bool lost = false;  // a wait ran out: this warp waits, loads and writes no more, but still sends
+    // A wait ran out: this warp goes through its rows without waiting, loading or sending, and writes none but bad ones.
+    // (It has not seen the others' pairs, so it does not know how many turns of a row they take: a pair too many would
+    // reach a CTA that has ended.  Those who miss its pairs are lost as well.)
+    bool lost = false;
     uint32_t loads = 0u;
     int turn = 0;
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, kProbs ? kResident : kResidentLogits
         if (turn == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         Pair* const buf = pairs[turn & 1];
         uint64_t* const bar = &sent[turn & 1];
-        if (lane < parts) {
+        if (lane < parts && !lost) {
             uint32_t dst, dst_bar;
             asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_u32(&buf[part * kWarps + warp])), "r"(lane));
             asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst_bar) : "r"(smem_u32(bar)), "r"(lane));
@@ -692,8 +695,11 @@ __global__ void __launch_bounds__(kThreads, kProbs ? kResident : kResidentLogits
     if constexpr (kProbs) {
         if (turn == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (lost) {
-            // its peers may still send: it stays until all have ended, and its own copy is here
+            // its peers may still send to this CTA: it stays until all of them have ended or are lost, then for the length
+            // of a wait (what they sent last is on its way, and nobody counts it), and until its own copy is here
             asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+            for (const long long t0 = clock64(); clock64() - t0 < kWaitBudgetCycles;) __nanosleep(1000);
+            __syncwarp();
             if (kStaged) (void)__all_sync(kAll, mbar_wait(&full[warp], (loads - 1u) & 1u));
         }
     }

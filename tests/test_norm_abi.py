@@ -139,6 +139,33 @@ def test_constrain_refuses(built_lib, kw, code):
     assert built_lib.infllmv2_constrain(*constrain_args(**kw)) == code
 
 
+def test_a_lost_warp_leaves_its_cluster_alone():
+    """A warp of a cluster whose bounded wait runs out has not seen the others' pairs, so it cannot know how many more of
+    its own they wait for, and pairs that they do not wait for would reach CTAs that have ended: it sends, loads and
+    writes nothing more, and its CTA stays until its peers are through and what they sent has arrived.  (A wait that
+    runs out cannot be provoked by a valid call.)"""
+    import os
+    import re
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "block_sparse_long_infllm_gb300",
+                        "csrc", "constrain.cu")
+    text = re.sub(r"//[^\n]*", "", open(path).read())
+    waits = [text[max(m.start() - 40, 0):m.start()] for m in re.finditer(r"\bmbar_(try_|test_)?wait\(", text)]
+    assert waits and all(w.rstrip().endswith("__all_sync(kAll,") for w in waits)
+    kernel = text[text.index("constrain_kernel("):text.index("cudaError_t launch_kind(")]
+    assert len(re.findall(r"st\.async", kernel)) == 1 and kernel.count("bulk_load(") == 1
+    exchange = kernel[kernel.index("const auto exchange"):kernel.index("while (row < to) {")]
+    sends = exchange[:exchange.index("st.async")]
+    assert sends.rstrip().split("if (")[-1].startswith("lane < parts && !lost)")
+    assert "if (!lost) wait(bar" in exchange and "if (tid == 0 && !lost) mbar_arrive_expect_tx(" in exchange
+    rows = kernel[kernel.index("while (row < to) {"):]
+    assert rows.count("fetch();") == 1 and "if (row < to && !lost) fetch();" in rows
+    assert rows.count("wait(&full[warp], loads++") == 1 and "if (!lost) wait(&full[warp], loads++" in rows
+    lost = rows[rows.rindex("if (lost) {"):]
+    stays = [lost.index(x) for x in ("barrier.cluster.arrive", "barrier.cluster.wait", "< kWaitBudgetCycles",
+                                     "mbar_wait(&full[warp]")]
+    assert stays == sorted(stays)
+
+
 def count_args(**kw):
     a = dict(tokens=at(1), lens=at(2), cu=None, B=4, T=8, total=0, V=1000, prompt=0, reset=0, history=at(3), ld=1000,
              stream=None)
