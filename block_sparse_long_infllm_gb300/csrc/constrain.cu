@@ -16,11 +16,12 @@
 // row's load overlaps the last one's way out.
 //
 // Measured on a GB300: 64 chains of 8 over 131072 fp32 logits with counts and a bias 150 us (3.7 TB/s; 108 us, 5.0
-// TB/s, without either: the counts cost about 12 of 39 instructions an element), one step of it (64 rows) 24.7;
-// adjusted logits alone 103; 2 trees of 16 over 32001 bf16 logits with masks 7.0; one row of 131072 5.7.  By CTA and
+// TB/s, without either: the counts cost about 12 of 39 instructions an element), one step of it (64 rows) 24.7; bf16
+// logits 159, to bf16 135; adjusted logits alone 103; 2 trees of 16 over 32001 bf16 logits with masks 7.0; one row of 131072 5.7.  By CTA and
 // CTAs per SM, the 64 chains: 256 threads, 2 CTAs 150; 192, 3: 160; 512, 2: 195.  With the cluster barrier instead
 // of counted stores 5 % more; values in registers instead of shared memory spilled; elements adjusted one unit at a
-// time, with the checks of what there is in the innermost loop, took 55 instructions an element and 200 us.
+// time, with the checks of what there is in the innermost loop, took 55 instructions an element and 200 us.  The kept
+// form's kernels by whole units spill a little at 128 registers: 40 bytes stored a thread for fp32, 24 for bf16.
 #include <float.h>
 #include <string.h>
 
@@ -42,8 +43,12 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kResident = 2;   // CTAs per SM
 constexpr int kResidentLogits = 3;  // the same of CTAs that keep nothing
 constexpr int kMaxCluster = 16;
-constexpr int kPiece = 2048;      // elements of a row that a warp keeps where a cluster's CTAs suffice,
-constexpr int kMostPiece = 6912;  // and at most (a CTA has 227 KB of shared memory)
+// Elements of a row that a warp keeps where a cluster's CTAs suffice, and at most (a CTA has 227 KB of shared memory).
+// Clusters are powers of two, so 8 CTAs keep rows of 65537 to 131072 and 16, of which fewer fit at once, longer ones:
+// 64 chains of 8 over 73448, 128256, 131072, 151936, 200064 take 112, 153, 150, 266, 320 us, their 64 rows alone 16,
+// 25, 25, 40, 47.
+constexpr int kPiece = 2048;
+constexpr int kMostPiece = 6912;
 constexpr int kSlice = kWarps * kPiece;
 constexpr int kStepValues = 8;        // elements that a lane takes in one step
 constexpr int kStepValuesStaged = 16; // the same out of shared memory, by whole units
@@ -767,7 +772,7 @@ cudaError_t launch(const ConstrainArgs& a) {
 
 // ---- token counts
 //
-// Measured: a prompt chunk's 4 x 4096 tokens marked 3.2 us (a launch); 64 sequences that start anew with prompts of up
+// Measured: a prompt chunk's 4 x 4096 tokens marked 3.2 us (a launch), a step's 64 x 8 tokens 2.3; 64 sequences that start anew with prompts of up
 // to 32768 tokens and 4096 generated ones, two launches, 15.6 us (17 MB of rows written: 2.5 at the copy rate; most of
 // the rest is the longest sequences' reading, 2.4 us a round of 8192 tokens, and two starts).  By compare-and-swap
 // on global memory it took 112 us (frequent tokens wait for one another), with tokens sent to their slices' CTAs

@@ -90,7 +90,7 @@ __device__ __forceinline__ Place place_of(const RopeArgs& a, int j) {
 // As in rope.cu: heads that a thread loads together, rows that a CTA takes at most, CTAs per SM.  us for the prompts
 // and the packed ones (bf16) by heads, rows, CTAs: 2, 16, 3 205, 49; 2, 32, 3 212, 47; 1, 16, 4 230, 61; 2, 16, 4
 // (spills) 245, 69; 3, 16, 3 222, 57; 3, 8, 3 247, 63; the next heads' loads under way while these are at work
-// (spills) 222 to 244.  16384 rows of fp32: 2, 8, 4 89.6; 2, 16, 3 102; 3, 4, 3 100.
+// (spills) 222 to 244.  (The kept form's bf16 kernels of many rows store 16 to 24 bytes a thread, too.)  16384 rows of fp32: 2, 8, 4 89.6; 2, 16, 3 102; 3, 4, 3 100.
 template <typename T>
 struct Plan;
 template <>
@@ -462,7 +462,8 @@ constexpr int kBackItems = 2;  // heads of a group of lanes, at least
 constexpr int kBackBatch = 16;  // rows of a batch, at most
 static_assert(kBackBatch <= kBackRows, "");
 // Heads that a thread loads together and CTAs per SM, by the rows' type.  (4096 rows and 16384 of fp32: 42.8 and 145
-// us; one head and 3 CTAs 45.5 and 160.  4096 of bf16: 31.3; two heads and 2 CTAs 33.9.)
+// us; one head and 3 CTAs 45.5 and 160.  4096 of bf16: 31.3; two heads and 2 CTAs 33.9.  Chunks, of bf16 rows, spill
+// at 80 registers: 56 to 96 bytes stored a thread; rows alone do not.)
 template <typename T>
 constexpr int kBackHeadsOf = sizeof(T) == 4 ? 2 : 1;
 template <typename T>
@@ -697,7 +698,9 @@ __global__ void __launch_bounds__(1024) norm_rope_weights(const float* parts, in
 
 template <int FORM, typename Tx, typename Tg, typename To, int D>
 cudaError_t launch_back_sized(const RopeArgs& a, const NormArgs& n) {
-    // rows of a batch: a divisor of the groups of lanes, or nearly so, and few where a row has many heads
+    // rows of a batch, fewer where a row has many heads.  With whole pairs there are 16 groups of lanes (32 for heads of
+    // 64): 5 rows have 3 each.  Without there are 8 (16): 5 rows have 1 each and 3 groups no row, and nothing is
+    // loaded ahead there (the chunk of 4096 tokens to bf16 with 18 to 126 rotated elements 65 us, with 128 37).
     const int heads = a.Hq + a.Hk + a.Hv, batch = heads <= 4 ? kBackBatch : heads <= 12 ? 8 : 5;
     // CTAs: all that fit at once, fewer where they would have less than kBackItems heads for each group of lanes
     const long long items = static_cast<long long>(a.rows) * heads, per_cta = kBackItems * kRopeThreads * 2 * kBackVec / D;

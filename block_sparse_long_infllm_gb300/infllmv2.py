@@ -602,7 +602,7 @@ def constrain(logits, out, tokens=None, tree_mask=None, n_nodes=None, history=No
     """Penalties, biases and masks on logits [B, n, V] (bf16 or fp32, rows may be further apart than V), and
     the distributions they leave, to out [B, n, V] (bf16 or fp32; it may be logits), as verify takes them;
     probs False: the logits themselves.  tokens, tree_mask and n_nodes as for verify (the drafts on a node's
-    way count as generated), history [B, V] int16 (count_tokens), allowed [B, n, W] int32 words of bits
+    way count as generated; tree_mask needs tokens), history [B, V] int16 (count_tokens), allowed [B, n, W] int32 words of bits
     (W >= ceil(V / 32)), bias [V] or [B, V] fp32, controls [B, 4] fp32: repetition, frequency, presence,
     temperature."""
     rc = (_native or _binding()).constrain(logits, out, tokens, tree_mask, n_nodes, history, allowed, bias, controls,
@@ -614,7 +614,8 @@ def constrain(logits, out, tokens=None, tree_mask=None, n_nodes=None, history=No
 def count_tokens(tokens, history, n_tokens=None, cu=None, prompt: bool = False, reset: bool = False, stream=None):
     """Adds tokens to history [B, V] int16, the counts that constrain reads (zeros at first): as generated
     ones, or as the prompt's.  tokens [B, T] int32, the first n_tokens [B] of each sequence (verify's
-    out_tokens and n_path), or packed [total] with cu [B + 1].  reset: the rows are cleared before."""
+    out_tokens and n_path), or packed [total] with cu [B + 1].  reset: the rows are cleared before (history[b:b + 1]:
+    of one slot; its rows start on 16 bytes if they are a multiple of 8 elements apart)."""
     rc = (_native or _binding()).count_tokens(tokens, history, n_tokens, cu, prompt, reset, stream)
     if rc != OK:
         raise InfLLMv2Error(rc, "infllmv2_count_tokens")

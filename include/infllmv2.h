@@ -565,7 +565,9 @@ int infllmv2_norm_rope_append_bwd(const float* dq, const float* dk, const float*
  * where it needs the row.
  *   logits, out   rows b*n_draft + i of ld, ld_out elements, dtype and out_dtype
  *                 INFLLMV2_BF16 or INFLLMV2_FP32; out may be logits (the same
- *                 pointer, ld and type) and overlaps nothing else
+ *                 pointer, ld and type) and overlaps nothing else.  Like every
+ *                 tensor they start on 16 bytes: the last row of a [T, V] tensor
+ *                 with an odd V may not, and is copied first
  *   tokens        [B, n_draft] int32, the drafts (a root's is not read); NULL: no
  *                 drafts are counted
  *   tree_mask     [B, n_draft] as for infllmv2_decode, given with tokens alone;
@@ -599,7 +601,8 @@ int infllmv2_constrain(const void* logits, int64_t ld, const int32_t* tokens, co
  *   cu != NULL: packed, sequence b's are tokens cu[b] .. cu[b+1] - 1 of total.
  * reset != 0: the rows of all B sequences are cleared before (a slot that another
  * sequence takes).  history rows are ld_history elements apart; what lies behind
- * their V counts is left as it is.
+ * their V counts is left as it is.  (With ld_history a multiple of 8 every row starts
+ * on 16 bytes, and a call can be given one slot's row alone.)
  * Device errors (a token outside [0, V), n_tokens outside [0, T], offsets that do
  * not ascend from 0 to at most total) set the error word; those tokens and the
  * tokens of such a length are left out, and of packed sequences each is taken
